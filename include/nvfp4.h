@@ -90,6 +90,9 @@ typedef enum { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 } nvfp4_out_dtype;
  * clears amax_out first). */
 typedef enum { NVFP4_EPI_NONE = 0, NVFP4_EPI_SWIGLU = 1 } nvfp4_epilogue;
 
+/* Output format of nvfp4_add_rmsnorm_quantize. */
+typedef enum { NVFP4_NORM_BF16 = 0, NVFP4_NORM_NVFP4 = 1, NVFP4_NORM_E4M3 = 2 } nvfp4_norm_format;
+
 /* Human-readable name of a status code (static string). */
 const char *nvfp4_status_string(int status);
 
@@ -474,6 +477,126 @@ nvfp4_status nvfp4_kv_dequantize(const uint8_t *k_q, const uint8_t *k_sf, const 
                                  const uint8_t *v_q, const uint8_t *v_sf, const float *v_gs,
                                  int64_t tokens, int64_t heads, int64_t head_dim,
                                  void *k_out, void *v_out, cudaStream_t stream);
+
+/*
+ * nvfp4_add_rmsnorm_quantize -- residual addition, RMS norm and the quantized
+ * input of the next projection in one pass over the rows.
+ * [P1: activations are quantized on the fly in front of the projections; P4:
+ *  the dense MLP takes NVFP4 activations, the attention projections FP8 ones.]
+ *   r = bf16(x + residual) (fp32 addition; r = x without a residual);
+ *   y = bf16(r * weight / sqrt(mean(r^2) + eps)), the correctly rounded value
+ *       (sum and root in 64 bits, one rounding);
+ *   format BF16   y only.
+ *   format NVFP4  q, sf = the bytes nvfp4_quantize writes for y in GIVEN mode.
+ *   format E4M3   scale[row] = max(max|y| / 448, 2^-126) (1 for a zero row),
+ *                 q = e4m3_rne_satfinite(y * (1 / scale[row])), each step one
+ *                 IEEE fp32 operation.
+ *   x, residual   bf16 [rows, ld], ld >= K, ld % 8 == 0, 16-byte aligned;
+ *                 residual nullable.
+ *   rows, K       rows < 2^31; K % 16 == 0 (K % 64 == 0 for MMA_TILED scales),
+ *                 K <= 65536.  rows == 0 is a no-op.
+ *   weight        bf16 [K], 16-byte aligned.  eps >= 0.
+ *   residual_out  nullable bf16 [rows, ld_ro]: receives r; may be x or residual
+ *                 itself (same address and stride), in place.
+ *   y             nullable (required for BF16) bf16 [rows, K], 16-byte aligned.
+ *   scale         NVFP4: fp32 [1], the given global scale (> 0); E4M3: fp32
+ *                 [rows], written.
+ *   q, sf         NVFP4: uint8 [rows, K/2] (roundup(rows,128) rows for
+ *                 MMA_TILED) and the scales in sf_layout; E4M3: uint8 [rows, K],
+ *                 sf unused.  q 16-byte aligned.
+ *   dev_status    NVFP4_ERR_NONFINITE when a y is NaN or inf (that row's codes
+ *                 are unspecified), NVFP4_ERR_INVALID_ARG for a bad global scale.
+ */
+nvfp4_status nvfp4_add_rmsnorm_quantize(const void *x, int64_t ld_x, const void *residual, int64_t ld_res,
+                                        int64_t rows, int64_t K, const void *weight, double eps,
+                                        void *residual_out, int64_t ld_ro, void *y, nvfp4_norm_format format,
+                                        float *scale, uint8_t *q, uint8_t *sf, nvfp4_sf_layout sf_layout,
+                                        int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Paged NVFP4 KV cache.  A pool of num_pages pages for K and one for V; a page
+ * holds page_size tokens (a multiple of 16) of every KV head, head-major:
+ *   k_q, v_q    uint8 [num_pages, heads, page_size, head_dim/2]
+ *   k_sf, v_sf  uint8 [num_pages, heads, page_size, head_dim/16] (E4M3)
+ * all 16-byte aligned, with one static fp32 global scale for K and one for V.
+ * A slot is page * page_size + row.  The rows are those of nvfp4_kv_quantize,
+ * so nvfp4_kv_dequantize reads a whole pool back (tokens = num_pages *
+ * page_size, the same heads and head_dim).
+ *
+ * nvfp4_kv_append -- rotate, quantize and write new tokens into their slots,
+ * and rotate the queries in the same call.  [P3: K and V are quantized to
+ *  NVFP4 when they are written to the cache.]
+ *   k, v          bf16 [tokens, heads, head_dim], token strides ld_k, ld_v (>=
+ *                 heads * head_dim, % 8 == 0, in elements: slices of a fused
+ *                 projection's output are fine), 16-byte aligned.
+ *   head_dim      % 32 == 0, 32..512.
+ *   slots         int64 [tokens]; a negative slot skips the token's K and V
+ *                 (padding); a slot past the pool skips them and reports
+ *                 NVFP4_ERR_INDEX.  The slots written must be distinct: two
+ *                 tokens with one slot leave either's elements there.
+ *   q, q_out      nullable bf16 [tokens, q_heads, head_dim], strides ld_q,
+ *                 ld_qo: rotated copy; q_out may be q itself, in place.
+ *   rope          fp32 [rope_rows, rot_dim]: per position rot_dim/2 cosines,
+ *                 then rot_dim/2 sines; 16-byte aligned.  rot_dim % 32 == 0,
+ *                 <= head_dim; 0 = no rotation (q is copied).
+ *   positions     int64 [tokens] (required with rot_dim > 0); one outside
+ *                 [0, rope_rows) skips the whole token and reports INDEX.
+ *   interleaved   0: element i pairs with i + rot_dim/2; 1: 2i with 2i + 1.
+ *                 (a, b) -> (a c - b s, b c + a s), correctly rounded to bf16.
+ *   k_gs, v_gs    fp32 [1], > 0: the encode is nvfp4_quantize's GIVEN mode.
+ *   dev_status    also NVFP4_ERR_NONFINITE: a 16-element block with a NaN or
+ *                 inf is stored as zeros, so that it cannot spread.
+ */
+nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void *v, int64_t ld_v, int64_t tokens, int heads,
+                             int head_dim, const int64_t *slots, const void *q, int64_t ld_q, int q_heads,
+                             void *q_out, int64_t ld_qo, const int64_t *positions, const float *rope,
+                             int64_t rope_rows, int rot_dim, int interleaved, const float *k_gs,
+                             const float *v_gs, uint8_t *k_q, uint8_t *k_sf, uint8_t *v_q, uint8_t *v_sf,
+                             int64_t num_pages, int page_size, int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * nvfp4_paged_attention -- attention over the paged NVFP4 cache.
+ * [P3: attention reads the NVFP4 KV cache and dequantizes it on the fly.]
+ *   O[t, h] = sum_j softmax_j(softmax_scale * q[t, h] . k_j) v_j over the cached
+ * tokens j that query t sees, with KV head h / (q_heads / kv_heads).
+ * The products are f16 x f16 with fp32 sums: K and V exactly (e2m1 * e4m3 is
+ * an f16), the softmax weights rounded to f16, the sums and the softmax in fp32.
+ *   q              bf16 [tokens, q_heads, head_dim], token stride ld_q (% 8).
+ *   query_offsets  nullable int32 [batch+1]: queries of sequence b are
+ *                  [query_offsets[b], query_offsets[b+1]); non-decreasing,
+ *                  within [0, tokens], at most max_query each, else nothing is
+ *                  computed and NVFP4_ERR_INDEX is reported.  NULL: one query
+ *                  per sequence (tokens == batch, max_query == 1).
+ *   seq_lens       int32 [batch]: cached tokens of each sequence, its queries'
+ *                  own tokens included; 0..max_pages * page_size (another value
+ *                  counts as 0 and is reported).
+ *   page_table     int32 [batch, max_pages]: page of tokens [i * page_size,
+ *                  (i+1) * page_size).  Entries past a sequence's length are not
+ *                  read.  A page outside [0, num_pages) is reported as INDEX and
+ *                  its tokens are left out of the sums.
+ *   causal         1: with n queries and length L, query j sees keys
+ *                  [0, L - n + j]; 0: all L.  A query that sees none gives a row
+ *                  of zeros (lse -inf).
+ *   head_dim       64, 128 or 256; q_heads a multiple of kv_heads; batch <= 4096.
+ *   out            fp32 or bf16 [tokens, q_heads, head_dim], 16-byte aligned.
+ *                  Rows outside every sequence's queries are left as they were.
+ *   lse            nullable fp32 [tokens, q_heads]: log(sum exp) of the scores.
+ *   workspace      >= nvfp4_paged_attention_workspace_size(...) bytes, 256-byte
+ *                  aligned, needs no clearing.  Calls that may overlap (other
+ *                  streams, other captured graphs) need workspaces of their own.
+ *   K and V elements of unused rows of a page may hold anything.
+ * The order of the sums depends only on the shapes and lengths: two calls with
+ * the same inputs give the same bits.
+ */
+size_t nvfp4_paged_attention_workspace_size(int batch, int64_t max_query, int q_heads, int kv_heads, int head_dim);
+nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, const int32_t *query_offsets,
+                                   int64_t max_query, const int32_t *seq_lens, int batch,
+                                   const int32_t *page_table, int max_pages, int q_heads, int kv_heads,
+                                   int head_dim, const uint8_t *k_q, const uint8_t *k_sf, const float *k_gs,
+                                   const uint8_t *v_q, const uint8_t *v_sf, const float *v_gs, int64_t num_pages,
+                                   int page_size, float softmax_scale, int causal, void *out,
+                                   nvfp4_out_dtype out_dtype, float *lse, void *workspace, int32_t *dev_status,
+                                   cudaStream_t stream);
 
 /*
  * nvfp4_moe_route -- routed (token, choice) pairs -> expert-grouped row order.

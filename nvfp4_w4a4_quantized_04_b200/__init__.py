@@ -10,9 +10,11 @@ Entry points (same names as the C ABI): ``nvfp4_quantize``,
 ``nvfp4_dequantize``, ``mxfp4_to_nvfp4``, ``mxfp4_quantize``, ``mxfp4_grouped_gemm``,
 ``nvfp4_grouped_gemm``,
 ``nvfp4_swiglu_quantize``, ``nvfp4_kv_quantize``, ``nvfp4_kv_dequantize``,
+``nvfp4_add_rmsnorm_quantize``, ``nvfp4_kv_append``, ``nvfp4_paged_attention``,
 ``nvfp4_moe_quantize``, ``nvfp4_moe_route``, ``nvfp4_moe_combine``,
 ``nvfp4_quantize_noalloc``, ``nvfp4_global_scale_from_amax``, plus ``nvfp4_workspace_size``,
-``nvfp4_padded_rows_bound`` and ``nvfp4_moe_route_workspace_size``.
+``nvfp4_padded_rows_bound``, ``nvfp4_moe_route_workspace_size`` and
+``nvfp4_paged_attention_workspace_size``.
 """
 from __future__ import annotations
 
@@ -41,6 +43,9 @@ OUT_BF16 = 1
 EPI_NONE = 0
 EPI_SWIGLU = 1
 GS_AMAX_GIVEN = 2
+NORM_BF16 = 0
+NORM_NVFP4 = 1
+NORM_E4M3 = 2
 
 EXPORTS = [
     "nvfp4_status_string", "nvfp4_workspace_size", "nvfp4_padded_rows_bound",
@@ -50,7 +55,8 @@ EXPORTS = [
     "nvfp4_gemm_select_kernel", "nvfp4_grouped_gemm_w4a16", "nvfp4_grouped_gemm_swiglu_nvfp4",
     "mxfp4_quantize", "mxfp4_grouped_gemm", "nvfp4_w4a16_workspace_size",
     "nvfp4_e2m1_encode", "nvfp4_e4m3_encode", "nvfp4_gemm_set_wait_budget", "nvfp4_global_scale_from_amax",
-    "nvfp4_w4a16_select_kernel",
+    "nvfp4_w4a16_select_kernel", "nvfp4_add_rmsnorm_quantize", "nvfp4_kv_append", "nvfp4_paged_attention",
+    "nvfp4_paged_attention_workspace_size",
 ]
 NOALLOC_MAX_GROUPS = 1024
 
@@ -122,6 +128,17 @@ def load_library(path: str = LIB_PATH):
     L.nvfp4_e4m3_encode.argtypes = [P, i64, P, P]
     L.nvfp4_global_scale_from_amax.restype = i32
     L.nvfp4_global_scale_from_amax.argtypes = [P, i64, ctypes.c_float, P, P, P]
+    L.nvfp4_add_rmsnorm_quantize.restype = i32
+    L.nvfp4_add_rmsnorm_quantize.argtypes = [P, i64, P, i64, i64, i64, P, ctypes.c_double, P, i64, P, i32, P, P, P,
+                                             i32, P, P]
+    L.nvfp4_kv_append.restype = i32
+    L.nvfp4_kv_append.argtypes = [P, i64, P, i64, i64, i32, i32, P, P, i64, i32, P, i64, P, P, i64, i32, i32, P, P,
+                                  P, P, P, P, i64, i32, P, P]
+    L.nvfp4_paged_attention_workspace_size.restype = ctypes.c_size_t
+    L.nvfp4_paged_attention_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    L.nvfp4_paged_attention.restype = i32
+    L.nvfp4_paged_attention.argtypes = [P, i64, i64, P, i64, P, i32, P, i32, i32, i32, i32, P, P, P, P, P, P, i64, i32,
+                                        ctypes.c_float, i32, P, i32, P, P, P, P]
     _lib = L
     return L
 
@@ -366,4 +383,48 @@ def nvfp4_moe_combine(y, y_dtype, rows, slot, weights, tokens, topk, H, out, out
         _stream(stream))
     if check:
         _check(st, "nvfp4_moe_combine")
+    return st
+
+
+def nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y, fmt, scale, q,
+                               sf, sf_layout=SF_ROWMAJOR, dev_status=None, stream=None, check=True) -> int:
+    """r = bf16(x + residual), y = RMS norm of r, and y quantized (``fmt``: NORM_BF16, NORM_NVFP4, NORM_E4M3)."""
+    st = load_library().nvfp4_add_rmsnorm_quantize(
+        _ptr(x), ld_x, _ptr(residual), ld_res, rows, K, _ptr(weight), eps, _ptr(residual_out), ld_ro, _ptr(y), fmt,
+        _ptr(scale), _ptr(q), _ptr(sf), sf_layout, _ptr(dev_status), _stream(stream))
+    if check:
+        _check(st, "nvfp4_add_rmsnorm_quantize")
+    return st
+
+
+def nvfp4_kv_append(k, ld_k, v, ld_v, tokens, heads, head_dim, slots, q, ld_q, q_heads, q_out, ld_qo, positions, rope,
+                    rope_rows, rot_dim, interleaved, k_gs, v_gs, k_q, k_sf, v_q, v_sf, num_pages, page_size,
+                    dev_status=None, stream=None, check=True) -> int:
+    """Rotate and quantize new tokens into their slots of a paged NVFP4 cache; rotate the queries."""
+    st = load_library().nvfp4_kv_append(
+        _ptr(k), ld_k, _ptr(v), ld_v, tokens, heads, head_dim, _ptr(slots), _ptr(q), ld_q, q_heads, _ptr(q_out), ld_qo,
+        _ptr(positions), _ptr(rope), rope_rows, rot_dim, interleaved, _ptr(k_gs), _ptr(v_gs), _ptr(k_q), _ptr(k_sf),
+        _ptr(v_q), _ptr(v_sf), num_pages, page_size, _ptr(dev_status), _stream(stream))
+    if check:
+        _check(st, "nvfp4_kv_append")
+    return st
+
+
+def nvfp4_paged_attention_workspace_size(batch: int, max_query: int, q_heads: int, kv_heads: int,
+                                         head_dim: int) -> int:
+    """Bytes of workspace of nvfp4_paged_attention (0 for shapes it refuses)."""
+    return int(load_library().nvfp4_paged_attention_workspace_size(batch, max_query, q_heads, kv_heads, head_dim))
+
+
+def nvfp4_paged_attention(q, ld_q, tokens, query_offsets, max_query, seq_lens, batch, page_table, max_pages, q_heads,
+                          kv_heads, head_dim, k_q, k_sf, k_gs, v_q, v_sf, v_gs, num_pages, page_size, softmax_scale,
+                          causal, out, out_dtype, lse, workspace, dev_status=None, stream=None, check=True) -> int:
+    """Attention of bf16 queries over a paged NVFP4 cache."""
+    st = load_library().nvfp4_paged_attention(
+        _ptr(q), ld_q, tokens, _ptr(query_offsets), max_query, _ptr(seq_lens), batch, _ptr(page_table), max_pages,
+        q_heads, kv_heads, head_dim, _ptr(k_q), _ptr(k_sf), _ptr(k_gs), _ptr(v_q), _ptr(v_sf), _ptr(v_gs), num_pages,
+        page_size, softmax_scale, causal, _ptr(out), out_dtype, _ptr(lse), _ptr(workspace), _ptr(dev_status),
+        _stream(stream))
+    if check:
+        _check(st, "nvfp4_paged_attention")
     return st

@@ -1,0 +1,756 @@
+// Attention over the paged NVFP4 cache: decode and few-query form (sm_100a).
+//
+//   O_r = sum_j softmax_j(scale q_r . k_j) v_j,   k_j = k_gs (e2m1 * e4m3),  v_j likewise,
+// over the keys that row r sees ("Qwen3.8-2.4T-A95B-NVFP4": the NVFP4 KV cache
+// is dequantized when attention reads it).  The cache is read at 4.5 bits an
+// element and never written out at 16.
+//
+// Rows.  The queries of a sequence and the heads of one KV group form rows
+// (row = query * group + head); a work item is (sequence, KV head, block of
+// 8 * NT rows), so the heads of a group share each read of K and V.
+//
+// What bounds it.  HBM: 9/16 byte an element of K and V against 4 operations
+// per row.  To reach that rate a 32-lane instruction may be spent on every
+// ~55 elements, which rules out anything but register dequantization, so:
+//  * S^T = K Q^T and O^T = V^T P^T run as mma.sync m16n8k16 with the cache as
+//    the A operand and 8 rows as N: a warp dequantizes its A fragments from
+//    the codes it reads (E2M1 -> f16 is one conversion per two codes, times
+//    the E4M3 scale as one f16x2 multiply; the product is exact in f16), and
+//    no dequantized value goes through shared memory.
+//  * K codes need no shuffling: a lane takes 16-byte pieces of its token's
+//    row, and the head dimension is permuted the same way on both operands.
+//    V is contracted over tokens, so pairs of tokens are interleaved at the
+//    nibble level (four logic operations per 16 codes) before the conversion.
+//  * P^T comes out of the first MMA as an accumulator with tokens as rows and
+//    turns into the second one's B operand by an 8x8 transpose (movmatrix).
+//  * Every warp has its own ring of cp.async stages (32 tokens of K and V) and
+//    its own softmax state; warps meet only at the end of an item.
+//  * The running maximum is raised only when a score exceeds it by more than
+//    2^8 (P stays below f16's range), so the usual step has one vote instead
+//    of a reduction and a rescale.
+// Q is brought to f16 by a power of two per row that puts the row's largest
+// element at 2^14: exact for every element within 2^29 of it.
+//
+// Split.  All items' steps (32 tokens each) form one line that is cut evenly
+// over the CTAs, so ragged batches, one long sequence and many short ones all
+// fill the GPU; an item that several CTAs share is joined by a second kernel
+// from (max, sum, unnormalized O) parts in the workspace.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "attention.cuh"
+#include "host_util.cuh"
+
+namespace nvfp4 {
+namespace attn {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 32;                // tokens per step
+constexpr int kLeast = kWarps;           // fewest steps per CTA: one per warp
+constexpr float kFloor = -1e30f;         // running maximum before the first key
+constexpr float kLazy = 8.0f;            // growth (log2) that P may show before a rescale
+constexpr int kMaxBatch = 4096;
+
+// ws_head: prefix[batch + 1], then steps per CTA.
+struct DecodeArgs {
+  Args a;
+  int32_t row_cap;      // sequences with more rows than this are left to the prefill kernel
+  int32_t *ws_head;
+  float *ws_ml;         // [2 * grid][R][2]
+  float *ws_o;          // [2 * grid][R][D]
+  int32_t grid;
+};
+
+// Steps of one item of a sequence and its number of row blocks; none when the
+// prefill kernel takes it.
+__device__ __forceinline__ void seq_shape(const DecodeArgs &P, const Seq &s, int R, int &steps, int &blocks) {
+  const int rows = s.queries * P.a.group;
+  const bool mine = rows <= P.row_cap;
+  blocks = mine ? (rows + R - 1) / R : 0;
+  steps = (mine && blocks) ? (s.len + kStep - 1) / kStep : 0;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Bytes of one half stage (16 tokens): K codes, V codes, K scales, V scales.
+template <int D> struct Half {
+  static constexpr int kCodes = 8 * D, kScales = D;
+  static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+};
+
+// Shared-memory byte offset of 16-byte piece c of token t's codes inside a half
+// stage.  K rows of 128 bytes swap halves on odd tokens, V lines of 128 bytes
+// rotate by token pair, so that the fragment reads below have no bank conflicts.
+template <int D>
+__device__ __forceinline__ int k_piece(int t, int c) {
+  if (D == 256) c ^= (t & 1) << 2;
+  return t * (D / 2) + c * 16;
+}
+template <int D>
+__device__ __forceinline__ int v_piece(int t, int c) {
+  const int pos = t * (D / 32) + c;                       // 16-byte position
+  const int sw = D == 64 ? ((t >> 2) & 1) << 1 : ((t >> 1) & 3) << 1;
+  return (pos ^ sw) * 16;
+}
+
+template <int D, int NT, int kStages>
+struct Layout {
+  static constexpr int R = 8 * NT;
+  static constexpr int kStageBytes = 2 * Half<D>::kBytes;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kRS = D + 20;                      // row stride of the O exchange, in floats
+  static constexpr int kO = kWarps * R * kRS * 4;
+  static constexpr int kMain = kRing > kO ? kRing : kO;
+  static constexpr int kQ = kMain;                        // Q fragments: NT * (D/16) * 32 lanes * 8 bytes
+  static constexpr int kRow = kQ + NT * (D / 16) * 256;   // per row: scale, limit
+  static constexpr int kMl = kRow + R * 8;                // per warp and row: max, sum
+  static constexpr int kScan = kMl + kWarps * R * 8;      // scan scratch
+  static constexpr int kPrefix = kScan + 64;
+  static constexpr int bytes(int batch) { return kPrefix + 4 * (batch + 2); }
+};
+
+template <int D, int NT, int kStages, int kMinCtas>
+__global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const DecodeArgs P) {
+  using L = Layout<D, NT, kStages>;
+  using H = Half<D>;
+  constexpr int R = L::R;
+  constexpr int J = D / 16;              // k-steps of S, m-tiles of O
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Args &A = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  float2 *s_row = reinterpret_cast<float2 *>(smem + L::kRow);
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kMl);
+  int32_t *s_scan = reinterpret_cast<int32_t *>(smem + L::kScan);
+  int32_t *s_prefix = reinterpret_cast<int32_t *>(smem + L::kPrefix);
+
+  // ---- prefix sums of the sequences' steps
+  {
+    const int per = (A.batch + kThreads - 1) / kThreads;
+    const int b0 = min(A.batch, tid * per), b1 = min(A.batch, b0 + per);
+    int local = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) bad |= !offsets_ok(A, b);
+    if (__syncthreads_or(bad)) {         // nothing is computed: the combine kernel sees 0 steps per CTA
+      if (blockIdx.x == 0 && tid == 0) {
+        P.ws_head[A.batch + 1] = 0;
+        report(A.dev_status, NVFP4_ERR_INDEX);
+      }
+      return;
+    }
+    for (int b = b0; b < b1; ++b) {
+      int steps, blocks;
+      seq_shape(P, load_seq(A, b), R, steps, blocks);
+      const int n = steps * blocks * A.heads_kv;
+      s_prefix[b] = n;
+      local += n;
+    }
+    int incl = local;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int run = incl - local;
+    for (int w = 0; w < warp; ++w) run += s_scan[w];
+    for (int b = b0; b < b1; ++b) {
+      const int n = s_prefix[b];
+      s_prefix[b] = run;
+      run += n;
+    }
+    if (tid == kThreads - 1) s_prefix[A.batch] = run;
+    __syncthreads();
+  }
+  const int total = s_prefix[A.batch];
+  const int per_cta = (int)kv::steps_per_cta(total, gridDim.x, kLeast);
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= A.batch; b += kThreads) P.ws_head[b] = s_prefix[b];
+    if (tid == 0) P.ws_head[A.batch + 1] = per_cta;
+  }
+  const float kgs = __ldg(A.k_gs), vgs = __ldg(A.v_gs);
+  int pos = (int)min((int64_t)total, (int64_t)blockIdx.x * per_cta);
+  const int end = (int)min((int64_t)total, (int64_t)pos + per_cta);
+  const uint32_t ring = smem_addr(smem) + warp * kStages * L::kStageBytes;
+  const uint32_t qs = smem_addr(smem + L::kQ) + lane * 8;
+
+  while (pos < end) {
+    const int b = upper_group(s_prefix, A.batch, pos);
+    const Seq seq = load_seq(A, b);
+    int steps, blocks;
+    seq_shape(P, seq, R, steps, blocks);
+    const int local = pos - s_prefix[b];
+    const int item = local / steps, s0 = local - item * steps;
+    const int head = item / blocks, block = item - head * blocks;
+    const int s1 = min(steps, s0 + (end - pos));
+    const int nrows = min(R, seq.queries * A.group - block * R);
+
+    // ---- Q fragments: one warp per row, f16 with a power of two per row
+    __syncthreads();
+    for (int r = warp; r < R; r += kWarps) {
+      constexpr int kPer = D / 32;
+      float v[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+      int limit = 0;
+      if (r < nrows) {
+        const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+        const uint16_t *p = A.q + (int64_t)(seq.first + qi) * A.ld_q + (int64_t)h * D + lane * kPer;
+        uint32_t w[kPer / 2];
+        if constexpr (kPer == 8) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(p);
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else if constexpr (kPer == 4) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(p);
+          w[0] = x.x; w[1] = x.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        limit = (int)kv::visible_keys(seq.len, seq.queries, qi, A.causal != 0);
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      top = __reduce_max_sync(0xffffffffu, top);
+      // 2^(14 - exponent of the row's largest element); 1 for zero, inf, NaN
+      // rows and subnormal ones (below 2^-112 the factor would leave fp32)
+      const int e = (int)(top >> 23);
+      const bool plain = e < 15 || e == 255;
+      const float up = plain ? 1.0f : __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - e) << 23);
+      const float down = plain ? 1.0f : __uint_as_float((uint32_t)max(1, 127 - 14 - 127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < kPer; i += (kPer >= 4 ? 4 : 2)) {
+        const int d = lane * kPer + i;
+        int tq, j;
+        if (D == 64) { tq = d >> 4; j = (d & 15) >> 2; }
+        else { const int c = d >> 5; tq = c & 3; j = (c >> 2) * 8 + ((d & 31) >> 2); }
+        uint8_t *dst = smem + L::kQ + (((r >> 3) * J + j) * 32 + (r & 7) * 4 + tq) * 8 + (d & 3) * 2;
+        if constexpr (kPer >= 4)
+          *reinterpret_cast<uint2 *>(dst) =
+              make_uint2(pack_f16x2(v[i] * up, v[i + 1] * up), pack_f16x2(v[i + 2] * up, v[i + 3] * up));
+        else
+          *reinterpret_cast<uint32_t *>(dst) = pack_f16x2(v[i] * up, v[i + 1] * up);
+      }
+      if (lane == 0) s_row[r] = make_float2(A.scale_log2 * kgs * kScaleFix * down, __int_as_float(limit));
+    }
+    __syncthreads();
+    float sc[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = s_row[8 * nt + 2 * t4 + i];
+        sc[nt][i] = x.x;
+        lim[nt][i] = __float_as_int(x.y);
+      }
+
+    float o[J][NT][4];
+#pragma unroll
+    for (int i = 0; i < J; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.0f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kFloor, l[nt][0] = l[nt][1] = 0.0f;
+
+    // ---- the warp's steps: s0 + warp, + kWarps, ...
+    const int mine = max(0, (s1 - s0 - warp + kWarps - 1) / kWarps);
+    int64_t base_reg = -1;               // lane i: pool row of half (i & 1) of iteration (block of 16) + i / 2
+    auto fetch_pages = [&](int it0) {
+      const int tok = (s0 + warp + (it0 + (lane >> 1)) * kWarps) * kStep + (lane & 1) * 16;
+      base_reg = -1;
+      if (it0 + (lane >> 1) < mine && tok < seq.len) {
+        const int e = tok / A.page_size;
+        const int32_t page = A.table[(int64_t)b * A.max_pages + e];
+        if (kv::page_ok(page, A.num_pages))
+          base_reg = kv::pool_row(page, A.heads_kv, A.page_size, head, tok - e * A.page_size);
+        else
+          report(A.dev_status, NVFP4_ERR_INDEX);
+      }
+    };
+    uint32_t valid = 0;                  // bit (2 * stage + half): the half was loaded
+    auto load_stage = [&](int it) {
+      if (it < mine) {
+        if ((it & 15) == 0) fetch_pages(it);
+        const int stage = it % kStages;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t base = __shfl_sync(0xffffffffu, base_reg, 2 * (it & 15) + h);
+          const uint32_t dst = ring + stage * L::kStageBytes + h * H::kBytes;
+          valid &= ~(1u << (2 * stage + h));
+          if (base >= 0) {
+            valid |= 1u << (2 * stage + h);
+            const uint8_t *kp = A.k_q + base * (D / 2), *vp = A.v_q + base * (D / 2);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              const int c = i * 32 + lane, t = c / (D / 32), pc = c % (D / 32);
+              cp_async16(dst + H::kK + k_piece<D>(t, pc), kp + c * 16);
+              cp_async16(dst + H::kV + v_piece<D>(t, pc), vp + c * 16);
+            }
+            if ((lane & 15) < D / 16) {
+              const bool is_v = lane >= 16;
+              cp_async16(dst + (is_v ? H::kVs : H::kKs) + (lane & 15) * 16,
+                         (is_v ? A.v_sf : A.k_sf) + base * (D / 16) + (lane & 15) * 16);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load_stage(i);
+
+    for (int it = 0; it < mine; ++it) {
+      load_stage(it + kStages - 1);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const int stage = it % kStages;
+      const uint32_t st = ring + stage * L::kStageBytes;
+      const int tok0 = (s0 + warp + it * kWarps) * kStep;
+
+      // S^T: tokens g and g + 8 of each half against the rows 2 t4, 2 t4 + 1
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t hb = st + h * H::kBytes;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[h][nt][k] = 0.0f;
+        constexpr int kPieces = D == 256 ? 2 : 1;
+#pragma unroll
+        for (int pc = 0; pc < kPieces; ++pc) {
+          uint32_t ka[4], kb[4], sa, sb;
+          if constexpr (D == 64) {
+            const uint2 x = lds_v2(hb + H::kK + g * 32 + t4 * 8), y = lds_v2(hb + H::kK + (g + 8) * 32 + t4 * 8);
+            ka[0] = x.x; ka[1] = x.y; kb[0] = y.x; kb[1] = y.y;
+            sa = lds_u8(hb + H::kKs + g * 4 + t4);
+            sb = lds_u8(hb + H::kKs + (g + 8) * 4 + t4);
+          } else {
+            const uint4 x = lds_v4(hb + H::kK + k_piece<D>(g, t4 + 4 * pc));
+            const uint4 y = lds_v4(hb + H::kK + k_piece<D>(g + 8, t4 + 4 * pc));
+            ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
+            kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
+            sa = lds_u16(hb + H::kKs + g * (D / 16) + 2 * (t4 + 4 * pc));
+            sb = lds_u16(hb + H::kKs + (g + 8) * (D / 16) + 2 * (t4 + 4 * pc));
+          }
+          constexpr int kWords = D == 64 ? 2 : 4;
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            const uint32_t fa = e4m3_pair_f16x2(__byte_perm(sa, 0, w < 2 ? 0x2020 : 0x2121));
+            const uint32_t fb = e4m3_pair_f16x2(__byte_perm(sb, 0, w < 2 ? 0x2020 : 0x2121));
+            const int j = pc * 8 + 2 * w;
+            const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(ka[w]), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(kb[w]), fb);
+            const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(ka[w]), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(kb[w]), fb);
+            const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(ka[w]), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(kb[w]), fb);
+            const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(ka[w]), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(kb[w]), fb);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q0 = lds_v2(qs + (nt * J + j) * 256), q1 = lds_v2(qs + (nt * J + j + 1) * 256);
+              mma_f16(s[h][nt], a0, a1, a2, a3, q0.x, q0.y);
+              mma_f16(s[h][nt], c0, c1, c2, c3, q1.x, q1.y);
+            }
+          }
+        }
+      }
+
+      // scores in log2 units, masked; does any exceed the running maximum by more than kLazy?
+      bool grow = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = (valid >> (2 * stage + h)) & 1;
+        const int t0 = tok0 + 16 * h + g;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = s[h][nt][k] * sc[nt][k & 1];
+            s[h][nt][k] = (ok && t0 + (k >> 1) * 8 < lim[nt][k & 1]) ? x : -INFINITY;
+            grow |= s[h][nt][k] > m[nt][k & 1] + kLazy;
+          }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, m[nt][i]);
+            const float f = ex2(m[nt][i] - x);
+            m[nt][i] = x;
+            l[nt][i] *= f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              o[j][nt][i] *= f;
+              o[j][nt][i + 2] *= f;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            p[k] = ex2(s[h][nt][k] - m[nt][k & 1]);
+            l[nt][k & 1] += p[k];
+          }
+          pb[h][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+          pb[h][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+        }
+
+      // O^T += V^T P^T: lane (g, t4) holds head elements [g D/8, (g+1) D/8) of tokens 2 t4, 2 t4 + 1, + 8, + 9
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t hb = st + h * H::kBytes;
+        constexpr int kWords = D / 64;
+        uint32_t v[4][kWords], vs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = 2 * t4 + (k & 1) + (k >> 1) * 8;
+          if constexpr (D == 256) {
+            const uint4 x = lds_v4(hb + H::kV + v_piece<D>(t, g));
+            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+            vs[k] = lds_u16(hb + H::kVs + t * 16 + 2 * g);
+          } else if constexpr (D == 128) {
+            const uint2 x = lds_v2(hb + H::kV + v_piece<D>(t, g >> 1) + (g & 1) * 8);
+            v[k][0] = x.x; v[k][1] = x.y;
+            vs[k] = lds_u8(hb + H::kVs + t * 8 + g);
+          } else {
+            v[k][0] = lds_u32(hb + H::kV + v_piece<D>(t, g >> 2) + (g & 3) * 4);
+            vs[k] = lds_u8(hb + H::kVs + t * 4 + (g >> 1));
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const int sel = w < 2 ? 0x6420 : 0x6521;
+          const uint32_t f01 = e4m3_pair_f16x2(__byte_perm(vs[0], vs[1], sel));
+          const uint32_t f23 = e4m3_pair_f16x2(__byte_perm(vs[2], vs[3], sel));
+          // bytes of (token, token + 1) nibble pairs: even head elements, odd head elements
+          const uint32_t e01 = (v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u);
+          const uint32_t d01 = ((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u);
+          const uint32_t e23 = (v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u);
+          const uint32_t d23 = ((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u);
+#define NVFP4_PV(B)                                                                                            \
+  {                                                                                                            \
+    const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<B>(e01), f01), a1 = mul_f16x2(e2m1x2_f16x2<B>(d01), f01);       \
+    const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<B>(e23), f23), a3 = mul_f16x2(e2m1x2_f16x2<B>(d23), f23);       \
+    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt)                                                          \
+        mma_f16(o[4 * w + B][nt], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);                                 \
+  }
+          NVFP4_PV(0) NVFP4_PV(1) NVFP4_PV(2) NVFP4_PV(3)
+#undef NVFP4_PV
+        }
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+
+    // ---- the four warps' states joined through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l[nt][i];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) s_ml[warp * R + 8 * nt + 2 * t4 + i] = make_float2(m[nt][i], x);
+      }
+    __syncthreads();                     // every warp is done with its ring
+    float *s_o = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float *p = s_o + (warp * R + 8 * nt + 2 * t4) * L::kRS + g * (D / 8 + 2) + 2 * j;
+        *reinterpret_cast<float2 *>(p) = make_float2(o[j][nt][0], o[j][nt][2]);
+        *reinterpret_cast<float2 *>(p + L::kRS) = make_float2(o[j][nt][1], o[j][nt][3]);
+      }
+    __syncthreads();
+    const bool whole = s0 == 0 && s1 == steps;
+    const int slot = 2 * blockIdx.x + kv::part_slot(blockIdx.x, per_cta, pos - s0);
+    for (int i = tid; i < nrows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      float2 ml[kWarps];
+      float M = kFloor;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) ml[w] = s_ml[w * R + r], M = fmaxf(M, ml[w].x);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(ml[w].x - M);
+        sum += f * ml[w].y;
+        const float *p = s_o + (w * R + r) * L::kRS + d + 2 * (d / (D / 8));
+        const float2 x = *reinterpret_cast<const float2 *>(p), y = *reinterpret_cast<const float2 *>(p + 2);
+        acc.x += f * x.x; acc.y += f * x.y; acc.z += f * y.x; acc.w += f * y.y;
+      }
+      if (whole) {
+        const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+        const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
+        const float f = sum == 0.0f ? 0.0f : vgs * kScaleFix / sum;
+        if (A.out_bf16) {
+          uint32_t lo, hi;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(acc.y * f), "f"(acc.x * f));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(acc.w * f), "f"(acc.z * f));
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + at * D + d) = make_uint2(lo, hi);
+        } else {
+          *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at * D + d) =
+              make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        }
+        if (A.lse && d == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4 *>(P.ws_o + ((int64_t)slot * R + r) * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2 *>(P.ws_ml + ((int64_t)slot * R + r) * 2) = make_float2(M, sum);
+      }
+    }
+    pos += s1 - s0;
+  }
+}
+
+// Joins the parts of an item that several CTAs shared, and writes zeros for
+// the rows of sequences without keys.  One CTA per row of an item: kGroups
+// groups of D/4 threads take every kGroups-th part.
+template <int D, int R>
+__global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P, int blocks_max) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ float4 s_o[256];
+  __shared__ float s_sum[kGroups], s_max[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Args &A = P.a;
+  const int tid = threadIdx.x, lane = tid % kLanes, part = tid / kLanes;
+  const int r = blockIdx.x % R;
+  int idx = blockIdx.x / R;
+  const int block = idx % blocks_max;
+  idx /= blocks_max;
+  const int head = idx % A.heads_kv, b = idx / A.heads_kv;
+  const Seq seq = load_seq(A, b);
+  int steps, blocks;
+  seq_shape(P, seq, R, steps, blocks);
+  if (block >= blocks || r >= seq.queries * A.group - block * R) return;
+  const int per = P.ws_head[A.batch + 1];
+  if (per == 0) return;                  // refused offsets
+  const int start = P.ws_head[b] + (head * blocks + block) * steps;
+  int c0 = 0, c1 = -1;
+  if (steps) {
+    c0 = start / per;
+    c1 = (start + steps - 1) / per;
+    if (c0 == c1) return;
+  }
+  float M = kFloor, sum = 0.0f;
+  for (int c = c0 + tid; c <= c1; c += 256) {
+    const int slot = 2 * c + kv::part_slot(c, per, start);
+    M = fmaxf(M, P.ws_ml[((int64_t)slot * R + r) * 2]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if ((tid & 31) == 0) s_max[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) M = fmaxf(M, s_max[k]);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int c = c0 + part; c <= c1; c += kGroups) {
+    const int64_t slot = (int64_t)(2 * c + kv::part_slot(c, per, start)) * R + r;
+    const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + slot * 2);
+    const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + slot * D + lane * 4);
+    const float f = ex2(ml.x - M);
+    sum += f * ml.y;
+    acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+  }
+  s_o[tid] = acc;
+  if (lane == 0) s_sum[part] = sum;
+  __syncthreads();
+  if (part) return;
+  sum = 0.0f;
+  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const float4 x = s_o[k * kLanes + lane];
+    sum += s_sum[k];
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  }
+  const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+  const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
+  const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
+  const int d = lane * 4;
+  if (A.out_bf16) {
+    uint32_t lo, hi;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(acc.y * f), "f"(acc.x * f));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(acc.w * f), "f"(acc.z * f));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + at * D + d) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at * D + d) =
+        make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+  }
+  if (A.lse && lane == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+}
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows per item for a call: the smallest block that holds every row of a
+// sequence, up to what the accumulators leave room for.
+int tiles_for(int64_t rows, int D) {
+  const int most = D == 256 ? 2 : 4;
+  if (rows <= 8) return 1;
+  if (rows <= 16 || most == 2) return 2;
+  return most;
+}
+
+// CTAs that the workspace is sized for: at most 4 per SM.
+int64_t max_grid() { return (int64_t)host::sm_count() * 4; }
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+template <int D, int NT, int kStages, int kMinCtas>
+nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t stream) {
+  using L = Layout<D, NT, kStages>;
+  auto kern = decode_kernel<D, NT, kStages, kMinCtas>;
+  const int smem = L::bytes(p.a.batch);
+  if (!host::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), L::bytes(kMaxBatch))) return NVFP4_ERR_CUDA;
+  int64_t grid = (int64_t)host::sm_count() * host::blocks_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
+  if (grid > max_grid()) grid = max_grid();
+  const int64_t want = (total_bound + kLeast - 1) / kLeast;
+  if (grid > want) grid = want < 1 ? 1 : want;
+  p.grid = (int32_t)grid;
+  p.ws_head = reinterpret_cast<int32_t *>(ws);
+  ws += align256(4 * ((int64_t)p.a.batch + 2));
+  p.ws_ml = reinterpret_cast<float *>(ws);
+  ws += align256(2 * max_grid() * L::R * 8);
+  p.ws_o = reinterpret_cast<float *>(ws);
+  kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
+  const int blocks_max = (int)(((int64_t)(p.a.max_query * (int64_t)p.a.group < p.row_cap ? p.a.max_query * (int64_t)p.a.group : p.row_cap) + L::R - 1) / L::R);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.a.batch * p.a.heads_kv * blocks_max * L::R));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, L::R>, p, blocks_max) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+}  // namespace attn
+}  // namespace nvfp4
+
+extern "C" {
+
+size_t nvfp4_paged_attention_workspace_size(int batch, int64_t max_query, int q_heads, int kv_heads, int head_dim) {
+  using namespace nvfp4::attn;
+  if (batch < 1 || batch > kMaxBatch || max_query < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  const int64_t R = 8 * tiles_for(max_query * (q_heads / kv_heads), head_dim);
+  return (size_t)(align256(4 * ((int64_t)batch + 2)) + align256(2 * max_grid() * R * 8) +
+                  align256(2 * max_grid() * R * head_dim * 4));
+}
+
+nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, const int32_t *query_offsets,
+                                   int64_t max_query, const int32_t *seq_lens, int batch, const int32_t *page_table,
+                                   int max_pages, int q_heads, int kv_heads, int head_dim, const uint8_t *k_q,
+                                   const uint8_t *k_sf, const float *k_gs, const uint8_t *v_q, const uint8_t *v_sf,
+                                   const float *v_gs, int64_t num_pages, int page_size, float softmax_scale,
+                                   int causal, void *out, nvfp4_out_dtype out_dtype, float *lse, void *workspace,
+                                   int32_t *dev_status, cudaStream_t stream) {
+  using namespace nvfp4;
+  using namespace nvfp4::attn;
+  if (batch < 0 || batch > kMaxBatch || tokens < 0 || tokens > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 4096) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (page_size < kv::kPageGranule || page_size % kv::kPageGranule != 0 || page_size > 65536 || max_pages < 0 ||
+      (int64_t)max_pages * page_size > 0x7FFFFFFF - 64 || num_pages < 0 || num_pages > 0x7FFFFFFF)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return NVFP4_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale < 1e30f)) return NVFP4_ERR_INVALID_ARG;
+  if (ld_q < (int64_t)q_heads * head_dim || ld_q % 8 != 0) return NVFP4_ERR_INVALID_ARG;
+  if (max_query < 1 || max_query > 0x7FFFFFFF / q_heads) return NVFP4_ERR_INVALID_ARG;
+  if (!query_offsets && (max_query != 1 || tokens != batch)) return NVFP4_ERR_INVALID_ARG;
+  if (batch == 0 || tokens == 0) return NVFP4_OK;
+  if (!q || !seq_lens || !out || !k_gs || !v_gs || !workspace || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(k_q, 16) || !aligned(k_sf, 16) || !aligned(v_q, 16) || !aligned(v_sf, 16) ||
+      !aligned(seq_lens, 4) || !aligned(query_offsets, 4) || !aligned(page_table, 4))
+    return NVFP4_ERR_INVALID_ARG;
+  if (max_pages > 0 && !page_table) return NVFP4_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!k_q || !k_sf || !v_q || !v_sf)) return NVFP4_ERR_INVALID_ARG;
+  const int group = q_heads / kv_heads;
+  const int64_t rows = max_query * group;
+  const int nt = tiles_for(rows, head_dim);
+  const int64_t blocks_max = (rows + 8 * nt - 1) / (8 * nt);
+  const int64_t steps_max = ((int64_t)max_pages * page_size + kStep - 1) / kStep;
+  // row blocks of all sequences: bounded by the queries there are and by max_query each
+  const int64_t by_tokens = tokens * group / (8 * nt) + batch;
+  const int64_t all_blocks = batch * blocks_max < by_tokens ? batch * blocks_max : by_tokens;
+  const int64_t total_bound = all_blocks * kv_heads * steps_max;
+  if (total_bound > 0x7FFFFFFF / 2 || (int64_t)batch * kv_heads * blocks_max * 8 * nt > 0x7FFFFFFF)
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  DecodeArgs p = {};
+  p.a.q = static_cast<const uint16_t *>(q);
+  p.a.ld_q = ld_q;
+  p.a.tokens = (int32_t)tokens;
+  p.a.offsets = query_offsets;
+  p.a.lens = seq_lens;
+  p.a.batch = batch;
+  p.a.max_query = (int32_t)max_query;
+  p.a.table = page_table;
+  p.a.max_pages = max_pages;
+  p.a.page_size = page_size;
+  p.a.num_pages = num_pages;
+  p.a.k_q = k_q; p.a.k_sf = k_sf; p.a.v_q = v_q; p.a.v_sf = v_sf;
+  p.a.k_gs = k_gs; p.a.v_gs = v_gs;
+  p.a.heads_q = q_heads; p.a.heads_kv = kv_heads; p.a.group = group;
+  p.a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.a.causal = causal;
+  p.a.out = out;
+  p.a.out_bf16 = out_dtype == NVFP4_OUT_BF16;
+  p.a.lse = lse;
+  p.a.dev_status = dev_status;
+  p.row_cap = 0x7FFFFFFF;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  if (head_dim == 64) {
+    if (nt == 1) return run<64, 1, 3, 4>(p, total_bound, ws, stream);
+    if (nt == 2) return run<64, 2, 3, 3>(p, total_bound, ws, stream);
+    return run<64, 4, 3, 2>(p, total_bound, ws, stream);
+  }
+  if (head_dim == 128) {
+    if (nt == 1) return run<128, 1, 3, 4>(p, total_bound, ws, stream);
+    if (nt == 2) return run<128, 2, 3, 3>(p, total_bound, ws, stream);
+    return run<128, 4, 3, 2>(p, total_bound, ws, stream);
+  }
+  if (nt == 1) return run<256, 1, 2, 2>(p, total_bound, ws, stream);
+  return run<256, 2, 2, 2>(p, total_bound, ws, stream);
+}
+
+}  // extern "C"

@@ -13,7 +13,9 @@ from typing import Optional
 
 import torch
 
-from . import (EPI_NONE, EPI_SWIGLU, GS_AMAX_GIVEN, GS_FROM_AMAX, GS_GIVEN, OUT_BF16, OUT_F32, SF_MMA_TILED, SF_ROWMAJOR,
+from . import (EPI_NONE, EPI_SWIGLU, GS_AMAX_GIVEN, GS_FROM_AMAX, GS_GIVEN, NORM_E4M3, NORM_NVFP4, OUT_BF16, OUT_F32,
+               SF_MMA_TILED, SF_ROWMAJOR, nvfp4_add_rmsnorm_quantize, nvfp4_kv_append, nvfp4_kv_dequantize,
+               nvfp4_paged_attention, nvfp4_paged_attention_workspace_size,
                mxfp4_grouped_gemm as _mxfp4_grouped_gemm, mxfp4_quantize as _mxfp4_quantize, mxfp4_to_nvfp4, nvfp4_dequantize, nvfp4_grouped_gemm, nvfp4_grouped_gemm_swiglu_nvfp4,
                nvfp4_global_scale_from_amax, nvfp4_grouped_gemm_w4a16, nvfp4_moe_combine,
                nvfp4_w4a16_workspace_size,
@@ -411,3 +413,226 @@ class MoELayer:
         with torch.cuda.graph(graph):
             out = self.forward(x, topk_ids, topk_weights, dev_status)
         return graph, out
+
+
+# ---------------------------------------------------------------- the norm in front of a projection
+def _rows(t: torch.Tensor, K: int, what: str):
+    """A bf16 [rows, K] operand with unit stride along K: its row stride."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != K or (t.stride(1) != 1 and K > 1):
+        raise ValueError(f"{what}: a bf16 [rows, {K}] tensor with contiguous rows is wanted")
+    return t.stride(0) if t.shape[0] > 1 else K
+
+
+def _norm_args(x, weight, residual, residual_out):
+    if x.dim() != 2:
+        raise ValueError("x: a bf16 [rows, K] tensor is wanted")
+    rows, K = x.shape
+    ld_x = _rows(x, K, "x")
+    if weight.dtype != torch.bfloat16 or weight.shape != (K,) or not weight.is_contiguous():
+        raise ValueError(f"weight: a contiguous bf16 [{K}] tensor is wanted")
+    ld_res = 0
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual: the shape of x is wanted")
+        ld_res = _rows(residual, K, "residual")
+    if residual_out is None and residual is not None:
+        residual_out = torch.empty((rows, K), dtype=torch.bfloat16, device=x.device)
+    ld_ro = 0
+    if residual_out is not None:
+        if residual_out.shape != x.shape:
+            raise ValueError("residual_out: the shape of x is wanted")
+        ld_ro = _rows(residual_out, K, "residual_out")
+    _same_device(x, weight, residual, residual_out)
+    return rows, K, ld_x, ld_res, residual_out, ld_ro
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch.Tensor, residual=None,
+                      eps: float = 1e-6, layout=SF_MMA_TILED, out: Optional[Packed] = None, residual_out=None,
+                      y=None, dev_status=None):
+    """r = x + residual, y = rmsnorm(r) * weight, and y as NVFP4 with the given
+    global scale (a calibrated ``input_scale``, fp32 [1]), in one pass.
+
+    Returns (packed y, r, y): r is ``residual_out`` (allocated when a residual
+    is given; may be ``residual`` itself) or x; y is the bf16 buffer passed as
+    ``y``, or None."""
+    rows, K, ld_x, ld_res, residual_out, ld_ro = _norm_args(x, weight, residual, residual_out)
+    if global_scale.dtype != torch.float32 or global_scale.numel() != 1:
+        raise ValueError("global_scale: an fp32 tensor of one element is wanted")
+    if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
+        raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
+    p = out if out is not None else empty_packed(rows, K, 1, None, layout, x.device)
+    if p.K != K or p.layout != layout or p.q.shape[0] < alloc_rows(rows, 1, False, layout):
+        raise ValueError("out: a packed tensor of this K and layout with enough rows is wanted")
+    _same_device(x, global_scale, y, p.q)
+    p.gs, p.offsets, p.num_groups, p.rows = global_scale, None, 1, rows
+    with torch.cuda.device(x.device):
+        nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
+                                   NORM_NVFP4, global_scale, p.q, p.sf, layout, dev_status)
+    return p, (residual_out if residual_out is not None else x), y
+
+
+def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6, q=None, scale=None,
+                     residual_out=None, y=None, dev_status=None):
+    """As add_rmsnorm_nvfp4 with an 8-bit output: (q uint8 [rows, K] E4M3 bytes,
+    scale fp32 [rows], r, y); q * scale[:, None] stands for y."""
+    rows, K, ld_x, ld_res, residual_out, ld_ro = _norm_args(x, weight, residual, residual_out)
+    if q is None:
+        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if q.element_size() != 1 or q.shape != x.shape or not q.is_contiguous():
+        raise ValueError("q: a contiguous one-byte tensor of x's shape is wanted")
+    if scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous():
+        raise ValueError("scale: fp32 [rows] is wanted")
+    if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
+        raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
+    _same_device(x, q, scale, y)
+    with torch.cuda.device(x.device):
+        nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
+                                   NORM_E4M3, scale, q, None, SF_ROWMAJOR, dev_status)
+    return q, scale, (residual_out if residual_out is not None else x), y
+
+
+# ---------------------------------------------------------------- the paged NVFP4 KV cache
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """fp32 [positions, rot_dim] for ``PagedKVCache.append``: per position the
+    rot_dim/2 cosines, then the sines, of position * base^(-2i/rot_dim); the
+    angles in 64 bits, so that far positions keep their digits."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * (base ** (-i / rot_dim))[None, :]
+    return torch.cat((angle.cos(), angle.sin()), 1).float().contiguous()
+
+
+def _heads(t: torch.Tensor, tokens, D: int, what: str):
+    """A bf16 [tokens, heads, D] operand whose heads of a token are contiguous: its token stride."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != D or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{what}: a bf16 [tokens, heads, {D}] tensor is wanted")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+class PagedKVCache:
+    """One attention layer's paged NVFP4 KV cache.
+
+    k_q, v_q: uint8 [num_pages, heads, page_size, D/2] codes; k_sf, v_sf: uint8
+    [num_pages, heads, page_size, D/16] scales; k_gs, v_gs: fp32 [1] static
+    global scales.  ``PagedKVCache.empty`` allocates them.  A slot is
+    page * page_size + row; the caller keeps the page tables."""
+
+    def __init__(self, k_q, k_sf, k_gs, v_q, v_sf, v_gs):
+        if k_q.dim() != 4:
+            raise ValueError("k_q: uint8 [num_pages, heads, page_size, D/2] is wanted")
+        self.num_pages, self.heads, self.page_size, half = k_q.shape
+        self.head_dim = D = 2 * half
+        for name, t, n in (("k_q", k_q, half), ("v_q", v_q, half), ("k_sf", k_sf, D // 16), ("v_sf", v_sf, D // 16)):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (*k_q.shape[:3], n) or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous uint8 {[*k_q.shape[:3], n]} tensor is wanted")
+        for name, t in (("k_gs", k_gs), ("v_gs", v_gs)):
+            if t.dtype != torch.float32 or t.numel() != 1:
+                raise ValueError(f"{name}: an fp32 tensor of one element is wanted")
+        _same_device(k_q, k_sf, k_gs, v_q, v_sf, v_gs)
+        self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs = k_q, k_sf, k_gs, v_q, v_sf, v_gs
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, k_gs: torch.Tensor, v_gs: torch.Tensor,
+              device="cuda") -> "PagedKVCache":
+        def u8(n):
+            return torch.empty((num_pages, heads, page_size, n), dtype=torch.uint8, device=device)
+        return cls(u8(head_dim // 2), u8(head_dim // 16), k_gs, u8(head_dim // 2), u8(head_dim // 16), v_gs)
+
+    def append(self, k, v, slots, q=None, q_out=None, positions=None, rope=None, interleaved: bool = False,
+               dev_status=None):
+        """Quantize k, v (bf16 [tokens, heads, D], the keys rotated to
+        ``positions`` by ``rope``) into ``slots`` (int64, negative = skip), and
+        return the rotated queries (``q_out``, allocated when not given; may be
+        q itself), or None without q."""
+        D, tokens = self.head_dim, k.shape[0]
+        ld_k, ld_v = _heads(k, None, D, "k"), _heads(v, tokens, D, "v")
+        if k.shape[1] != self.heads or v.shape[1] != self.heads:
+            raise ValueError(f"k, v: {self.heads} heads are wanted")
+        if slots.dtype != torch.int64 or slots.shape != (tokens,) or not slots.is_contiguous():
+            raise ValueError("slots: a contiguous int64 [tokens] tensor is wanted")
+        rot = rows = 0
+        if rope is not None:
+            if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+                raise ValueError("rope: a contiguous fp32 [positions, rot_dim] tensor is wanted")
+            rows, rot = rope.shape
+            if positions is None or positions.dtype != torch.int64 or positions.shape != (tokens,) or \
+                    not positions.is_contiguous():
+                raise ValueError("positions: a contiguous int64 [tokens] tensor is wanted")
+        ld_q = ld_qo = hq = 0
+        if q is not None:
+            ld_q, hq = _heads(q, tokens, D, "q"), q.shape[1]
+            if q_out is None:
+                q_out = torch.empty((tokens, hq, D), dtype=torch.bfloat16, device=q.device)
+            ld_qo = _heads(q_out, tokens, D, "q_out")
+            if q_out.shape != q.shape:
+                raise ValueError("q_out: the shape of q is wanted")
+        _same_device(self.k_q, k, v, slots, q, q_out, positions, rope)
+        with torch.cuda.device(self.k_q.device):
+            nvfp4_kv_append(k, ld_k, v, ld_v, tokens, self.heads, D, slots, q, ld_q, hq, q_out, ld_qo, positions, rope,
+                            rows, rot, int(interleaved), self.k_gs, self.v_gs, self.k_q, self.k_sf, self.v_q,
+                            self.v_sf, self.num_pages, self.page_size, dev_status)
+        return q_out if q is not None else None
+
+    def workspace(self, batch: int, max_query: int, q_heads: int) -> torch.Tensor:
+        """A workspace for ``attend`` calls of up to these sizes on one stream."""
+        n = nvfp4_paged_attention_workspace_size(batch, max_query, q_heads, self.heads, self.head_dim)
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=self.k_q.device)
+
+    def attend(self, q, seq_lens, page_table, query_offsets=None, max_query: int = 1, softmax_scale=None,
+               causal: bool = True, out=None, out_dtype=OUT_BF16, lse=None, ws=None, dev_status=None):
+        """Attention of q (bf16 [tokens, q_heads, D]) over the cache.
+
+        seq_lens int32 [batch]: cached tokens, the queries' own included;
+        page_table int32 [batch, pages]; query_offsets int32 [batch + 1] (None:
+        one query per sequence) with at most ``max_query`` queries each; lse:
+        fp32 [tokens, q_heads] to fill.  Returns out [tokens, q_heads, D]."""
+        D = self.head_dim
+        ld_q = _heads(q, None, D, "q")
+        tokens, hq = q.shape[0], q.shape[1]
+        if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+            raise ValueError("seq_lens: a contiguous int32 [batch] tensor is wanted")
+        batch = seq_lens.shape[0]
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or \
+                not page_table.is_contiguous():
+            raise ValueError("page_table: a contiguous int32 [batch, pages] tensor is wanted")
+        if query_offsets is not None and (query_offsets.dtype != torch.int32 or query_offsets.shape != (batch + 1,) or
+                                          not query_offsets.is_contiguous()):
+            raise ValueError("query_offsets: a contiguous int32 [batch + 1] tensor is wanted")
+        dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+        if out is None:
+            out = torch.empty((tokens, hq, D), dtype=dt, device=q.device)
+        elif out.dtype != dt or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out: a contiguous {dt} tensor of q's shape is wanted")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous()):
+            raise ValueError("lse: a contiguous fp32 [tokens, q_heads] tensor is wanted")
+        if ws is None:
+            ws = self.workspace(batch, max_query, hq)
+        _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws)
+        if ws.numel() * ws.element_size() < nvfp4_paged_attention_workspace_size(batch, max_query, hq, self.heads, D):
+            raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
+        scale = D ** -0.5 if softmax_scale is None else softmax_scale
+        with torch.cuda.device(self.k_q.device):
+            nvfp4_paged_attention(q, ld_q, tokens, query_offsets, max_query, seq_lens, batch, page_table,
+                                  page_table.shape[1], hq, self.heads, D, self.k_q, self.k_sf, self.k_gs, self.v_q,
+                                  self.v_sf, self.v_gs, self.num_pages, self.page_size, scale, int(causal), out,
+                                  out_dtype, lse, ws, dev_status)
+        return out
+
+    def dequantize(self):
+        """The whole pool back in bf16: (k, v), each [num_pages, heads, page_size, D]."""
+        shape = (*self.k_q.shape[:3], self.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
+        with torch.cuda.device(self.k_q.device):
+            nvfp4_kv_dequantize(self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs,
+                                self.num_pages * self.page_size, self.heads, self.head_dim, k, v)
+        return k, v
