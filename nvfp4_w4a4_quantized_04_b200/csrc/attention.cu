@@ -6,8 +6,9 @@
 // element and never written out at 16.
 //
 // Rows.  The queries of a sequence and the heads of one KV group form rows
-// (row = query * group + head); a work item is (sequence, KV head, block of
-// 8 * NT rows), so the heads of a group share each read of K and V.
+// (row = query * group + head); a work item is (sequence, KV head) with its up
+// to 8 * NT rows, so the heads of a group share each read of K and V.
+// Sequences with more rows go to the prefill form (attention_prefill.cu).
 //
 // What bounds it.  HBM: 9/16 byte an element of K and V against 4 operations
 // per row.  To reach that rate a 32-lane instruction may be spent on every
@@ -40,6 +41,7 @@
 #include <stdint.h>
 
 #include "attention.cuh"
+#include "attention_internal.cuh"
 #include "host_util.cuh"
 
 namespace nvfp4 {
@@ -49,9 +51,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                // tokens per step
 constexpr int kLeast = kWarps;           // fewest steps per CTA: one per warp
-constexpr float kFloor = -1e30f;         // running maximum before the first key
-constexpr float kLazy = 8.0f;            // growth (log2) that P may show before a rescale
-constexpr int kMaxBatch = 4096;
 
 // ws_head: prefix[batch + 1], then steps per CTA.
 struct DecodeArgs {
@@ -63,13 +62,12 @@ struct DecodeArgs {
   int32_t grid;
 };
 
-// Steps of one item of a sequence and its number of row blocks; none when the
-// prefill kernel takes it.
-__device__ __forceinline__ void seq_shape(const DecodeArgs &P, const Seq &s, int R, int &steps, int &blocks) {
-  const int rows = s.queries * P.a.group;
-  const bool mine = rows <= P.row_cap;
-  blocks = mine ? (rows + R - 1) / R : 0;
-  steps = (mine && blocks) ? (s.len + kStep - 1) / kStep : 0;
+// Steps of one item (sequence, KV head); false when the prefill form takes the
+// sequence or it has no queries.
+__device__ __forceinline__ bool seq_steps(const DecodeArgs &P, const Seq &s, int &steps) {
+  const bool mine = s.queries > 0 && s.queries * P.a.group <= P.row_cap;
+  steps = mine ? (s.len + kStep - 1) / kStep : 0;
+  return mine;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -153,9 +151,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
       return;
     }
     for (int b = b0; b < b1; ++b) {
-      int steps, blocks;
-      seq_shape(P, load_seq(A, b), R, steps, blocks);
-      const int n = steps * blocks * A.heads_kv;
+      int steps;
+      seq_steps(P, load_seq(A, b), steps);
+      const int n = steps * A.heads_kv;
       s_prefix[b] = n;
       local += n;
     }
@@ -192,13 +190,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
   while (pos < end) {
     const int b = upper_group(s_prefix, A.batch, pos);
     const Seq seq = load_seq(A, b);
-    int steps, blocks;
-    seq_shape(P, seq, R, steps, blocks);
+    int steps;
+    seq_steps(P, seq, steps);
     const int local = pos - s_prefix[b];
-    const int item = local / steps, s0 = local - item * steps;
-    const int head = item / blocks, block = item - head * blocks;
+    const int head = local / steps, s0 = local - head * steps;
     const int s1 = min(steps, s0 + (end - pos));
-    const int nrows = min(R, seq.queries * A.group - block * R);
+    const int nrows = seq.queries * A.group;
 
     // ---- Q fragments: one warp per row, f16 with a power of two per row
     __syncthreads();
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
       for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
       int limit = 0;
       if (r < nrows) {
-        const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+        const int qi = r / A.group, h = head * A.group + r - qi * A.group;
         const uint16_t *p = A.q + (int64_t)(seq.first + qi) * A.ld_q + (int64_t)h * D + lane * kPer;
         uint32_t w[kPer / 2];
         if constexpr (kPer == 8) {
@@ -232,12 +229,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
 #pragma unroll
       for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       top = __reduce_max_sync(0xffffffffu, top);
-      // 2^(14 - exponent of the row's largest element); 1 for zero, inf, NaN
-      // rows and subnormal ones (below 2^-112 the factor would leave fp32)
-      const int e = (int)(top >> 23);
-      const bool plain = e < 15 || e == 255;
-      const float up = plain ? 1.0f : __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - e) << 23);
-      const float down = plain ? 1.0f : __uint_as_float((uint32_t)max(1, 127 - 14 - 127 + e) << 23);
+      float up, down;
+      row_power((int)(top >> 23), up, down);
 #pragma unroll
       for (int i = 0; i < kPer; i += (kPer >= 4 ? 4 : 2)) {
         const int d = lane * kPer + i;
@@ -283,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
       const int tok = (s0 + warp + (it0 + (lane >> 1)) * kWarps) * kStep + (lane & 1) * 16;
       base_reg = -1;
       if (it0 + (lane >> 1) < mine && tok < seq.len) {
-        const int e = tok / A.page_size;
+        const int e = (int)fast_div((uint32_t)tok, A.by_page);
         const int32_t page = A.table[(int64_t)b * A.max_pages + e];
         if (kv::page_ok(page, A.num_pages))
           base_reg = kv::pool_row(page, A.heads_kv, A.page_size, head, tok - e * A.page_size);
@@ -515,18 +508,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
         acc.x += f * x.x; acc.y += f * x.y; acc.z += f * y.x; acc.w += f * y.y;
       }
       if (whole) {
-        const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+        const int qi = r / A.group, h = head * A.group + r - qi * A.group;
         const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
         const float f = sum == 0.0f ? 0.0f : vgs * kScaleFix / sum;
-        if (A.out_bf16) {
-          uint32_t lo, hi;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(acc.y * f), "f"(acc.x * f));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(acc.w * f), "f"(acc.z * f));
-          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + at * D + d) = make_uint2(lo, hi);
-        } else {
-          *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at * D + d) =
-              make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-        }
+        store_out(A, at, D, d, acc, f);
         if (A.lse && d == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
       } else {
         *reinterpret_cast<float4 *>(P.ws_o + ((int64_t)slot * R + r) * D + d) = acc;
@@ -541,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
 // the rows of sequences without keys.  One CTA per row of an item: kGroups
 // groups of D/4 threads take every kGroups-th part.
 template <int D, int R>
-__global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P, int blocks_max) {
+__global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
   __shared__ float4 s_o[256];
   __shared__ float s_sum[kGroups], s_max[8];
@@ -549,17 +534,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P, int bl
   const Args &A = P.a;
   const int tid = threadIdx.x, lane = tid % kLanes, part = tid / kLanes;
   const int r = blockIdx.x % R;
-  int idx = blockIdx.x / R;
-  const int block = idx % blocks_max;
-  idx /= blocks_max;
+  const int idx = blockIdx.x / R;
   const int head = idx % A.heads_kv, b = idx / A.heads_kv;
   const Seq seq = load_seq(A, b);
-  int steps, blocks;
-  seq_shape(P, seq, R, steps, blocks);
-  if (block >= blocks || r >= seq.queries * A.group - block * R) return;
+  int steps;
+  if (!seq_steps(P, seq, steps) || r >= seq.queries * A.group) return;
   const int per = P.ws_head[A.batch + 1];
   if (per == 0) return;                  // refused offsets
-  const int start = P.ws_head[b] + (head * blocks + block) * steps;
+  const int start = P.ws_head[b] + head * steps;
   int c0 = 0, c1 = -1;
   if (steps) {
     c0 = start / per;
@@ -599,37 +581,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P, int bl
     sum += s_sum[k];
     acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
   }
-  const int row = block * R + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+  const int qi = r / A.group, h = head * A.group + r - qi * A.group;
   const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
   const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
   const int d = lane * 4;
-  if (A.out_bf16) {
-    uint32_t lo, hi;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(acc.y * f), "f"(acc.x * f));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(acc.w * f), "f"(acc.z * f));
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + at * D + d) = make_uint2(lo, hi);
-  } else {
-    *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at * D + d) =
-        make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-  }
+  store_out(A, at, D, d, acc, f);
   if (A.lse && lane == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Rows per item for a call: the smallest block that holds every row of a
-// sequence, up to what the accumulators leave room for.
-int tiles_for(int64_t rows, int D) {
-  const int most = D == 256 ? 2 : 4;
-  if (rows <= 8) return 1;
-  if (rows <= 16 || most == 2) return 2;
-  return most;
-}
+// Most rows of a sequence that the decode form takes (one row block: the
+// accumulators leave room for no more, and a second block would read the cache
+// again); sequences with more go to the prefill form.
+int row_limit(int D) { return D == 256 ? 16 : 32; }
+
+// 8-row tiles of a row block that holds `rows` rows.
+int tiles_for(int64_t rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
 
 // CTAs that the workspace is sized for: at most 4 per SM.
 int64_t max_grid() { return (int64_t)host::sm_count() * 4; }
 
-int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t decode_workspace(int batch, int64_t rows, int D) {
+  const int64_t R = 8 * tiles_for(rows, D);
+  return align256(4 * ((int64_t)batch + 2)) + align256(2 * max_grid() * R * 8) + align256(2 * max_grid() * R * D * 4);
+}
 
 template <int D, int NT, int kStages, int kMinCtas>
 nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t stream) {
@@ -649,9 +625,8 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   p.ws_o = reinterpret_cast<float *>(ws);
   kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
-  const int blocks_max = (int)(((int64_t)(p.a.max_query * (int64_t)p.a.group < p.row_cap ? p.a.max_query * (int64_t)p.a.group : p.row_cap) + L::R - 1) / L::R);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.a.batch * p.a.heads_kv * blocks_max * L::R));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.a.batch * p.a.heads_kv * L::R));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -659,7 +634,7 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, L::R>, p, blocks_max) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, L::R>, p) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 }  // namespace attn
@@ -672,9 +647,9 @@ size_t nvfp4_paged_attention_workspace_size(int batch, int64_t max_query, int q_
   if (batch < 1 || batch > kMaxBatch || max_query < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  const int64_t R = 8 * tiles_for(max_query * (q_heads / kv_heads), head_dim);
-  return (size_t)(align256(4 * ((int64_t)batch + 2)) + align256(2 * max_grid() * R * 8) +
-                  align256(2 * max_grid() * R * head_dim * 4));
+  const int64_t rows = max_query * (q_heads / kv_heads);
+  return (size_t)(decode_workspace(batch, rows, head_dim) +
+                  (rows > row_limit(head_dim) ? prefill_workspace(batch, max_query, q_heads / kv_heads, head_dim) : 0));
 }
 
 nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, const int32_t *query_offsets,
@@ -707,14 +682,14 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   if (num_pages > 0 && (!k_q || !k_sf || !v_q || !v_sf)) return NVFP4_ERR_INVALID_ARG;
   const int group = q_heads / kv_heads;
   const int64_t rows = max_query * group;
-  const int nt = tiles_for(rows, head_dim);
-  const int64_t blocks_max = (rows + 8 * nt - 1) / (8 * nt);
-  const int64_t steps_max = ((int64_t)max_pages * page_size + kStep - 1) / kStep;
-  // row blocks of all sequences: bounded by the queries there are and by max_query each
-  const int64_t by_tokens = tokens * group / (8 * nt) + batch;
-  const int64_t all_blocks = batch * blocks_max < by_tokens ? batch * blocks_max : by_tokens;
-  const int64_t total_bound = all_blocks * kv_heads * steps_max;
-  if (total_bound > 0x7FFFFFFF / 2 || (int64_t)batch * kv_heads * blocks_max * 8 * nt > 0x7FFFFFFF)
+  const int cap = row_limit(head_dim);
+  // steps of the whole call: row blocks are bounded by the queries that there
+  // are; the longest line is the prefill form's with 64-key tiles
+  const int64_t keys = (int64_t)max_pages * page_size;
+  const int64_t steps_max = (keys + kStep - 1) / kStep;
+  const int64_t blocks = tokens * group / 128 + batch;
+  if ((int64_t)batch * kv_heads * steps_max > 0x3FFFFFFF || blocks * kv_heads * (keys / 64 + 1) > 0x3FFFFFFF ||
+      (int64_t)batch * ((rows + 127) / 128) > 0x3FFFFFFF)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   DecodeArgs p = {};
   p.a.q = static_cast<const uint16_t *>(q);
@@ -727,6 +702,7 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.a.table = page_table;
   p.a.max_pages = max_pages;
   p.a.page_size = page_size;
+  p.a.by_page = make_fastdiv((uint32_t)page_size);
   p.a.num_pages = num_pages;
   p.a.k_q = k_q; p.a.k_sf = k_sf; p.a.v_q = v_q; p.a.v_sf = v_sf;
   p.a.k_gs = k_gs; p.a.v_gs = v_gs;
@@ -737,8 +713,16 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.a.out_bf16 = out_dtype == NVFP4_OUT_BF16;
   p.a.lse = lse;
   p.a.dev_status = dev_status;
-  p.row_cap = 0x7FFFFFFF;
+  p.row_cap = cap;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
+  if (rows > cap) {
+    // a single sequence has one form only; a batch may hold both kinds
+    const nvfp4_status st =
+        launch_prefill(p.a, head_dim, batch == 1 ? 0 : cap, ws + decode_workspace(batch, rows, head_dim), stream);
+    if (st != NVFP4_OK || batch == 1) return st;
+  }
+  const int nt = tiles_for(rows, head_dim);
+  const int64_t total_bound = (int64_t)batch * kv_heads * steps_max;
   if (head_dim == 64) {
     if (nt == 1) return run<64, 1, 3, 4>(p, total_bound, ws, stream);
     if (nt == 2) return run<64, 2, 3, 3>(p, total_bound, ws, stream);

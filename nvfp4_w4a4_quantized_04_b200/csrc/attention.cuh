@@ -19,6 +19,7 @@ struct Args {
   int32_t batch, max_query;
   const int32_t *table;        // [batch, max_pages]
   int32_t max_pages, page_size;
+  FastDiv by_page;             // division by page_size
   int64_t num_pages;
   const uint8_t *k_q, *k_sf, *v_q, *v_sf;
   const float *k_gs, *v_gs;

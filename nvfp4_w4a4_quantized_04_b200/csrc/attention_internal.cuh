@@ -1,0 +1,44 @@
+// What the decode and the prefill form of the paged attention share on top of
+// attention.cuh: constants, the row scaling of Q, the output store, and the
+// prefill launcher that attention.cu calls.
+#pragma once
+
+#include "attention.cuh"
+
+namespace nvfp4 {
+namespace attn {
+
+constexpr float kFloor = -1e30f;         // running maximum before the first key
+constexpr float kLazy = 8.0f;            // growth (log2) that P may show before a rescale
+constexpr int kMaxBatch = 4096;
+
+// The power of two that brings a row of Q to f16: 2^(14 - e) for a row whose
+// largest element has biased exponent e; 1 for zero, inf, NaN rows and for
+// rows below 2^-112, where the factor would leave fp32.
+__device__ __forceinline__ void row_power(int e, float &up, float &down) {
+  const bool plain = e < 15 || e == 255;
+  up = plain ? 1.0f : __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+  down = plain ? 1.0f : __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+// Four output elements times f at (row `at`, element d).
+__device__ __forceinline__ void store_out(const Args &A, int64_t at, int D, int d, float4 acc, float f) {
+  if (A.out_bf16) {
+    uint32_t lo, hi;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(acc.y * f), "f"(acc.x * f));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(acc.w * f), "f"(acc.z * f));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + at * D + d) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at * D + d) =
+        make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+  }
+}
+
+inline int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Prefill form: sequences with more than row_floor rows.
+int64_t prefill_workspace(int batch, int64_t max_query, int group, int D);
+nvfp4_status launch_prefill(const Args &a, int D, int row_floor, uint8_t *ws, cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace nvfp4

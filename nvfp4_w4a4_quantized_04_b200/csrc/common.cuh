@@ -127,6 +127,20 @@ __device__ inline bool load_groups(const int32_t *__restrict__ group_offsets, in
   return true;
 }
 
+// n / d for 32-bit n by a multiply-high, with the constants of Granlund and
+// Montgomery, "Division by invariant integers using multiplication" (1994):
+// l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, q = (mulhi(n, m) + n) >> l.
+struct FastDiv { uint32_t d, m, l; };
+inline FastDiv make_fastdiv(uint32_t d) {
+  uint32_t l = 0;
+  while (l < 32 && (1ull << l) < d) ++l;
+  const uint64_t m = (((1ull << 32) * ((1ull << l) - d)) / d) + 1;
+  return FastDiv{d, (uint32_t)m, l};
+}
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv &f) {
+  return (uint32_t)(((uint64_t)__umulhi(n, f.m) + n) >> f.l);
+}
+
 // Largest g in [0, G) with a[g] <= x (a non-decreasing, a[0] <= x).
 __device__ __forceinline__ int upper_group(const int32_t *a, int G, int64_t x) {
   int lo = 0, hi = G - 1;

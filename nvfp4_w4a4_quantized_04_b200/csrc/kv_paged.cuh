@@ -59,5 +59,13 @@ NVFP4_HD int64_t steps_per_cta(int64_t total, int64_t grid, int64_t least) {
 // each kind, so two slots a CTA are enough.
 NVFP4_HD int part_slot(int64_t c, int64_t per, int64_t first) { return c * per < first ? 1 : 0; }
 
+// Steps [lo, hi) of an item in CTA c's range [c * per, (c+1) * per) of a line
+// on which the item takes `fixed` units from `start` and then one per step.
+NVFP4_HD void item_part(int64_t c, int64_t per, int64_t start, int fixed, int steps, int &lo, int &hi) {
+  const int64_t a = c * per - start - fixed, b = a + per;
+  lo = (int)(a < 0 ? 0 : a > steps ? steps : a);
+  hi = (int)(b < 0 ? 0 : b > steps ? steps : b);
+}
+
 }  // namespace kv
 }  // namespace nvfp4

@@ -149,20 +149,6 @@ __global__ void finalize_scales_kernel(const uint32_t *__restrict__ amax_bits, i
 }
 
 // ---------------------------------------------------------------- pass 2: encode
-// n / d for 32-bit n by a multiply-high, with the constants of Granlund and
-// Montgomery, "Division by invariant integers using multiplication" (1994):
-// l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1, q = (mulhi(n, m) + n) >> l.
-struct FastDiv { uint32_t d, m, l; };
-FastDiv make_fastdiv(uint32_t d) {
-  uint32_t l = 0;
-  while (l < 32 && (1ull << l) < d) ++l;
-  const uint64_t m = (((1ull << 32) * ((1ull << l) - d)) / d) + 1;
-  return FastDiv{d, (uint32_t)m, l};
-}
-__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv &f) {
-  return (uint32_t)(((uint64_t)__umulhi(n, f.m) + n) >> f.l);
-}
-
 // Gathered long rows (row_index, K >= 2048): one warp per result row, the
 // row's group and source row looked up once, up to 8 blocks (256 bytes) in
 // flight per lane; warps stride over rows so the grid streams through the

@@ -422,6 +422,14 @@ ATTEND = [
     (256, 1, 8, 128, [260], [17], False),
     (128, 4, 4, 64, [99, 64], [6, 64], False),
     (64, 1, 2, 16, [31, 77], [2, 7], False),
+    # sequences on both sides of the row limit between the two forms, in one batch
+    (256, 2, 8, 64, [300, 1000, 64, 5, 0, 129], [1, 200, 2, 5, 3, 3], True),
+    (128, 2, 4, 48, [300, 1000, 64, 513, 9], [8, 9, 1, 400, 9], True),
+    (64, 1, 16, 16, [130, 2000, 17], [2, 3, 17], True),
+    # many row blocks and tiles, shared between CTAs
+    (128, 1, 4, 64, [6000], [257], True),
+    (256, 1, 2, 64, [9000, 200], [130, 65], True),
+    (64, 2, 1, 32, [700, 1500], [700, 1400], True),
 ]
 
 
@@ -510,6 +518,17 @@ def test_attention_bad_pages_lengths_and_offsets():
     assert st.item() == nv.ERR_INDEX
     want, _, mag = c.reference(skip={0: slice(32, 48), 1: slice(0, 16)})
     assert ((out.double() - want).abs() <= c.tolerance(want, mag, torch.float32)).all()
+    # the same with many queries a sequence
+    for D in (64, 128, 256):
+        c = Case(8, D, 2, 4, 16, [300, 290], [150, 60], True)
+        table = c.table.clone()
+        table[0, 2], table[0, 17], table[1, 0] = c.cache.num_pages, 1 << 30, -1
+        st = status_word()
+        out = c.run(page_table=table, out_dtype=L.OUT_F32, dev_status=st)
+        assert st.item() == nv.ERR_INDEX
+        want, _, mag = c.reference(skip={0: list(range(32, 48)) + list(range(272, 288)), 1: list(range(16))})
+        assert ((out.double() - want).abs() <= c.tolerance(want, mag, torch.float32)).all()
+    c = Case(7, 128, 2, 4, 16, [100, 90], None, True)
     for bad in (-1, c.table.shape[1] * 16 + 1, 1 << 30):
         lens = c.seq_lens.clone()
         lens[0] = bad

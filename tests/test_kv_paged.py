@@ -23,6 +23,9 @@ int ok_page(int page, long long pages) { return page_ok(page, pages); }
 long long visible(long long len, long long q, long long j, int causal) { return visible_keys(len, q, j, causal != 0); }
 long long per(long long total, long long grid, long long least) { return steps_per_cta(total, grid, least); }
 int slot_of(long long c, long long per, long long first) { return part_slot(c, per, first); }
+void part_of(long long c, long long per, long long start, int fixed, int steps, int *lo, int *hi) {
+  item_part(c, per, start, fixed, steps, *lo, *hi);
+}
 }
 """
 
@@ -43,6 +46,8 @@ def host(tmp_path_factory):
     L.visible.argtypes = [i64, i64, i64, ctypes.c_int]
     L.per.argtypes = [i64, i64, i64]
     L.slot_of.argtypes = [i64, i64, i64]
+    L.part_of.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int),
+                          ctypes.POINTER(ctypes.c_int)]
     return L
 
 
@@ -107,6 +112,36 @@ def test_work_split_covers_every_step_once(host, seed):
         c0, c1 = first // per, (first + n - 1) // per
         want = [] if c0 == c1 else [(c, host.slot_of(c, per, first)) for c in range(c0, c1 + 1)]
         assert parts.get(first, []) == want
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_weighted_split_covers_every_step_once(host, seed):
+    """The same for a line on which every item takes a fixed cost before its steps."""
+    r = random.Random(100 + seed)
+    fixed, items, at = r.choice((0, 1, 2, 5)), [], 0
+    for _ in range(r.randrange(1, 60)):
+        n = r.choice((1, 2, 3, 17, 100, 700))
+        items.append((at, n))
+        at += n + fixed
+    grid = r.choice((1, 2, 7, 148))
+    per = host.per(at, grid, 1)
+    lo, hi = ctypes.c_int(), ctypes.c_int()
+    parts, slots = {}, set()
+    for c in range(grid):
+        for start, n in items:
+            host.part_of(c, per, start, fixed, n, lo, hi)
+            inside = start < (c + 1) * per and start + fixed + n > c * per
+            assert inside or lo.value >= hi.value
+            if lo.value < hi.value:
+                parts.setdefault(start, []).append((c, lo.value, hi.value))
+                if hi.value - lo.value < n:
+                    key = (c, host.slot_of(c, per, start))
+                    assert key not in slots
+                    slots.add(key)
+    for start, n in items:
+        got = parts[start]
+        assert [p[1] for p in got] == [0] + [p[2] for p in got][:-1] and got[-1][2] == n
+        assert [p[0] for p in got] == list(range((start + fixed) // per, (start + fixed + n - 1) // per + 1))
 
 
 # ------------------------------------------------------------------ refusals
