@@ -703,6 +703,7 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.a.max_pages = max_pages;
   p.a.page_size = page_size;
   p.a.by_page = make_fastdiv((uint32_t)page_size);
+  p.a.by_group = make_fastdiv((uint32_t)group);
   p.a.num_pages = num_pages;
   p.a.k_q = k_q; p.a.k_sf = k_sf; p.a.v_q = v_q; p.a.v_sf = v_sf;
   p.a.k_gs = k_gs; p.a.v_gs = v_gs;

@@ -24,6 +24,7 @@ struct Args {
   const uint8_t *k_q, *k_sf, *v_q, *v_sf;
   const float *k_gs, *v_gs;
   int32_t heads_q, heads_kv, group;
+  FastDiv by_group;            // division by group
   float scale_log2;            // softmax scale * log2(e)
   int32_t causal;
   void *out;                   // [tokens, q_heads, D]

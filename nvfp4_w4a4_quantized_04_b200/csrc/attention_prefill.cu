@@ -5,25 +5,33 @@
 // every key, so the products are what bounds it, and they run on the 5th
 // generation tensor cores:
 //   S [128 rows, T keys]  = Q K^T    tcgen05.mma kind::f16, A = Q in tensor memory,
-//   O [128 rows, D]      += P V      A = P in tensor memory,
+//   O [128 rows, D]      += P V      A = P in tensor or shared memory,
 // with K and V dequantized to f16 (exactly) once per tile into shared memory.
 //
 // Roles of a CTA (one per SM):
-//  * warps 0-7, softmax: two threads per row, each with half of a tile's keys.
-//    They put Q into tensor memory (f16, a power of two per row), turn S into P
-//    (f16, written over their own half of S), keep the running maximum and sum,
-//    and store O at the end of an item.  The maximum is raised, and O in tensor
-//    memory rescaled, only when a score exceeds it by more than 2^8.
-//  * warps 8-15, converters: cache codes -> f16 tiles in shared memory in a
-//    ring of six 16 or 32 KB buffers (K and V in turn).  A warp takes 8 tokens
-//    x 4 sixteen-byte pieces at a time: the 16-byte shared stores of 8 lanes
-//    fall on the 8 different positions of the 128-byte swizzle.  K and V tiles
-//    have one layout, [64-element chunk][token][128 bytes]: K-major for S (keys
-//    are N) and N-major for O (keys are K), so V needs no transposition.  The
-//    codes of a tile are loaded a whole tile ahead of their conversion, and the
-//    page ids a tile ahead of that.
-//  * warp 16, one thread issues the MMAs: S of tile i + 1 goes ahead of P V of
-//    tile i, so the tensor cores work while the softmax runs.
+//  * warps 0-7, softmax: two threads per row, each with 64 keys of a 128-key
+//    tile.  They read S into registers at once, which frees it for the next
+//    tile's MMAs, turn it into P (f16), keep the running maximum and sum, put Q
+//    into tensor memory (f16, a power of two per row) at the start of an item and
+//    store O at its end.  A tile's weights are taken by the maximum as it stands,
+//    without looking for a larger one first; only when their sum exceeds 2^13 are
+//    they taken again and O in tensor memory rescaled.
+//  * warps 8-23, converters: cache codes -> f16 tiles in shared memory in a
+//    ring of four units of 32 KB (16 KB with D = 64).  A unit of K is 128 tokens x
+//    up to 128 elements, a unit of V up to 256 elements of 64 or 128 tokens, both
+//    as [64-element chunk][token][128 bytes]: K-major for S (keys are N) and
+//    N-major for O (keys are K), so V needs no transposition.
+//  * warp 25, loader: codes and scales by bulk copies, several tiles ahead.  (As
+//    ordinary loads of 16 bytes a lane from 8 rows they took 1290 of the about
+//    1680 wavefronts a 64-key tile that kept the load/store pipe 77 % busy; begun
+//    by each converter warp for itself, the copies' issue was half of its time.)
+//  * warp 24, one thread issues the MMAs: as soon as S of tile i is read, S of a
+//    later tile, and when P of tile i is there, P V, without waiting for any MMA
+//    in between.  P lies apart from S, with D = 256 in shared memory (tensor
+//    memory is full): where it was written over S, the next S had to wait for
+//    P V, and the tensor cores idled through both waits.
+// A tile has 128 keys because an S MMA costs about 56 cycles with N = 64 keys
+// and little more with N = 128.
 // Keeping Q in tensor memory instead of shared memory halves what the first
 // product reads from shared memory, whose bandwidth the converters' stores and
 // the B operands already fill (256 cycles each for K and V, stored and read,
@@ -49,32 +57,45 @@ using gemm::tc_fence_before;
 
 constexpr int kRows = 128;
 constexpr int kPlanThreads = 1024;
-constexpr int kSoft = 8, kConv = 8;           // softmax and converter warps
-constexpr int W_CONV = kSoft, W_MMA_P = kSoft + kConv;
-constexpr int kPreThreads = (W_MMA_P + 4) * 32;   // five warpgroups; the last has one working warp
+constexpr int kSoft = 8, kConv = 16;          // softmax and converter warps
+constexpr int W_CONV = kSoft, W_MMA_P = kSoft + kConv, W_LOAD = W_MMA_P + 1;
+constexpr int kPreThreads = (W_MMA_P + 4) * 32;   // seven warpgroups; the last has two working warps
 // Registers per thread after the roles part (setmaxnreg moves them between
-// warpgroups): 256 x 128 + 256 x 80 + 128 x 56 = 60416 of the 640 x 96 = 61440
-// that the block is launched with.
-constexpr int kLaunchRegs = 96, kSoftRegs = 128, kConvRegs = 80, kRestRegs = 56;
+// warpgroups): 256 x 136 + 512 x 48 + 128 x 40 = 64512, the 896 x 72 that the
+// block is launched with.
+constexpr int kLaunchRegs = 72, kSoftRegs = 136, kConvRegs = 48, kRestRegs = 40;
 static_assert(32 * (kSoft * kSoftRegs + kConv * kConvRegs + 4 * kRestRegs) <= kPreThreads * kLaunchRegs, "registers");
-constexpr int kBufs = 6;
 // What an item costs besides its tiles (Q in, the first S, O out), in tiles:
 // the line that is cut over the CTAs counts it, so that a CTA with many short
 // items takes no longer than the others.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 5;
+// A tile's weights may add up to this before the maximum is raised: every
+// weight then is an f16 (65504 is the largest).
+constexpr float kMostSum = 8192.0f;
 
 template <int D> struct Pre {
-  static constexpr int T = D == 256 ? 64 : 128;         // keys per tile
-  static constexpr int kTile = T * D * 2;               // bytes of one f16 tile
+  static constexpr int T = 128;                         // keys per tile
+  static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K or V tile
+  static constexpr int kUnit = T * D * 2 / kUnits;      // bytes of one
+  static constexpr int kBufs = 4;                       // units in the ring
+  static constexpr bool kPShared = D == 256;            // P in shared memory, else in tensor memory
+  static constexpr int kSBufs = D == 256 ? 1 : 2;       // S tiles in tensor memory
   static constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;   // tensor memory columns
+  static constexpr uint32_t kP = kS + kSBufs * T;       // (unless shared)
   static constexpr uint32_t kCols = 512;
-  static constexpr int kBar = kBufs * kTile;
-  // kv_full[6], kv_empty[6], s_full[2], p_full[2], pv_done, o_done, q_ready, drain
-  static constexpr int kNumBars = 2 * kBufs + 2 + 2 + 4;
-  static constexpr int kMisc = kBar + kNumBars * 8;      // tmem base, abort flag, bad-page tags[8]
-  static constexpr int kXch = kMisc + 8 + 32;            // [2][2][128] floats between a row's two threads
-  static constexpr int kBytes = kXch + 2 * 2 * kRows * 4 + 1024;
-  static_assert(kS + 2 * T <= kCols, "tensor memory");
+  static constexpr int kPAt = kBufs * kUnit;
+  static constexpr int kPBytes = kPShared ? kRows * T * 2 : 0;
+  // codes and scales of tiles on their way
+  static constexpr int kSlots = D == 256 ? 3 : 6;
+  static constexpr int kCodeBytes = T * D / 2, kScaleBytes = T * D / 16, kSlotBytes = kCodeBytes + kScaleBytes;
+  static constexpr int kStageAt = kPAt + kPBytes;
+  static constexpr int kBar = kStageAt + kSlots * kSlotBytes;
+  // kv_full[], kv_empty[], s_full[2], s_free[2], pv_done[2], p_full, o_done, q_ready, drain, staged[], unstaged[]
+  static constexpr int kNumBars = 2 * kBufs + 2 + 2 + 2 + 4 + 2 * kSlots;
+  static constexpr int kMisc = kBar + kNumBars * 8;      // tmem base, abort flag, bad-page tags[16]
+  static constexpr int kXch = kMisc + 8 + 64;            // [4][128] floats between a row's two threads
+  static constexpr int kBytes = kXch + 4 * kRows * 4 + 1024;
+  static_assert(kS + kSBufs * T + (kPShared ? 0 : T / 2) <= kCols, "tensor memory");
   static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -82,6 +103,7 @@ struct PlanArgs {
   Args a;
   int32_t row_floor;       // sequences with at most this many rows are left to the decode kernel
   int32_t tile;
+  int32_t chunk;           // tokens per bulk copy: a power of two that divides the tile and the page
   int32_t grid;
   int32_t *count;          // [0] entries, [1] cost per CTA, [2] total cost
   int32_t *prefix;         // [entries + 1] cost of all heads before entry e: (tiles + kItemCost) each
@@ -191,6 +213,7 @@ struct Segment {
 
 struct Walk {
   int pos, end, entry, per;
+  int item_end = 0, cost = 0;          // of the item before; its entry's last head
   __device__ __forceinline__ Walk(const PlanArgs &P) {
     per = P.count[1];
     const int total = P.count[2];
@@ -200,66 +223,76 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const PlanArgs &P, Segment &g) {
     while (pos < end) {
-      while (P.prefix[entry + 1] <= pos) ++entry;
-      const int2 e = P.entry[entry];
-      const int base = P.prefix[entry];
-      const int cost = (P.prefix[entry + 1] - base) / P.a.heads_kv;
-      g.steps = cost - kItemCost;
-      g.head = (pos - base) / cost;
-      g.item_start = base + g.head * cost;
+      if (cost && pos == item_end && g.head + 1 < P.a.heads_kv) {
+        ++g.head;                      // the next head of the same rows: nothing to look up
+        g.item_start = pos;
+      } else {
+        while (P.prefix[entry + 1] <= pos) ++entry;
+        const int2 e = P.entry[entry];
+        const int base = P.prefix[entry];
+        cost = (P.prefix[entry + 1] - base) / P.a.heads_kv;
+        g.steps = cost - kItemCost;
+        g.head = (pos - base) / cost;
+        g.item_start = base + g.head * cost;
+        g.b = e.x;
+        g.block = e.y;
+        g.seq = load_seq(P.a, e.x);
+        g.nrows = min(kRows, g.seq.queries * P.a.group - g.block * kRows);
+      }
       kv::item_part(blockIdx.x, per, g.item_start, kItemCost, g.steps, g.s0, g.s1);
-      pos = min(end, g.item_start + cost);
-      if (g.s0 >= g.s1) continue;      // only the item's fixed cost falls into this range
-      g.b = e.x;
-      g.block = e.y;
-      g.seq = load_seq(P.a, e.x);
-      g.nrows = min(kRows, g.seq.queries * P.a.group - g.block * kRows);
-      return true;
+      item_end = g.item_start + cost;
+      pos = min(end, item_end);
+      if (g.s0 < g.s1) return true;    // else only the item's fixed cost falls into this range
     }
     return false;
   }
 };
 
-// 64 columns of this warp's lanes, complete on return.
-__device__ __forceinline__ void tm_ld64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
-      "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr) : "memory");
-}
-
-__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Columns of this warp's lanes.  tm_ld32 and tm_ld16 are complete on return;
+// tm_ld_begin only starts the load and tm_ld_end, which names the registers,
+// completes it.
+__device__ __forceinline__ void tm_ld_begin(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr) : "memory");
 }
-
-__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_ld_end(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+__device__ __forceinline__ void tm_ld_begin(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr) : "memory");
 }
+__device__ __forceinline__ void tm_ld_end(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
 
-__device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  tm_ld_begin(taddr, r);
+  tm_ld_end(r);
+}
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  tm_ld_begin(taddr, r);
+  tm_ld_end(r);
+}
+
+__device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t *v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
@@ -271,6 +304,14 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&v)[32])
 }
 
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      :: "r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -312,26 +353,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Column of P's k-th 16 keys in a tile's S buffer: each half of the keys lies
-// at the start of its half of S.
-template <int T>
-__device__ __forceinline__ uint32_t p_col(int k) {
-  constexpr int kHalf = T / 32;                           // 16-key steps per half
-  return (k / kHalf) * (T / 2) + (k % kHalf) * 8;
-}
-
 // Barrier of the two warps that share 32 rows.
 __device__ __forceinline__ void pair_sync(int quadrant) {
   asm volatile("bar.sync %0, 64;" :: "r"(1 + quadrant) : "memory");
 }
-
-template <int N>
-__device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 64) tm_ld64(taddr, r);
-  else tm_ld32(taddr, r);
-}
-
-// N / 2 columns of packed f16 pairs.
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -339,42 +364,87 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16])
          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t (&v)[N]) {
-  if constexpr (N == 32) tm_st32(taddr, v);
-  else tm_st16(taddr, v);
+
+// One lane of the (whole) warp.  With elect.sync the compiler keeps the MMA
+// operands in uniform registers; behind `lane == 0` every MMA issue cost about
+// 110 cycles, more than the MMA itself.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// 64 scores from token `tok0` on: those past the row's limit, and with `bad`
+// those of tokens on bad pages, to -inf.
+__device__ __forceinline__ void mask_scores(const Args &A, const Segment &G, uint32_t (&s)[2][32], int left, int tok0,
+                                            bool bad) {
+#pragma unroll
+  for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < left ? s[k >> 5][k & 31] : 0xFF800000u;
+  if (bad) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (tok0 + k < G.seq.len &&
+          !kv::page_ok(__ldg(A.table + (int64_t)G.b * A.max_pages + fast_div((uint32_t)(tok0 + k), A.by_page)),
+                       A.num_pages)) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (j == k) s[j >> 5][j & 31] = 0xFF800000u;
+      }
+  }
+}
+
+// The weights exp2(s sc - m) of 64 scores as packed f16 pairs, and their fp32 sum.
+__device__ __forceinline__ float weights(const uint32_t (&s)[2][32], float sc, float m, uint32_t (&p)[32]) {
+  const uint64_t sc2 = pair_f32(sc, sc), neg_m = pair_f32(-m, -m);
+  uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const uint32_t *x = &s[k >> 4][2 * (k & 15)];
+    const uint64_t v = fma_f32x2(((uint64_t)x[1] << 32) | x[0], sc2, neg_m);
+    const float a = ex2(__uint_as_float((uint32_t)v)), b = ex2(__uint_as_float((uint32_t)(v >> 32)));
+    if (k & 1) sum1 = add_f32x2(sum1, pair_f32(a, b));
+    else sum0 = add_f32x2(sum0, pair_f32(a, b));
+    p[k] = pack_f16x2(a, b);
+  }
+  sum0 = add_f32x2(sum0, sum1);
+  return __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
 }
 
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs P) {
   using L = Pre<D>;
-  constexpr int T = L::T;
+  constexpr int T = L::T, kBufs = L::kBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const Args &A = P.a;
   const uint32_t sbase = smem_addr(smem);
   const uint32_t kv_full = sbase + L::kBar, kv_empty = kv_full + 8 * kBufs, s_full = kv_empty + 8 * kBufs;
-  const uint32_t p_full = s_full + 16, pv_done = p_full + 16, o_done = pv_done + 8, q_ready = o_done + 8;
-  const uint32_t drain = q_ready + 8;
+  const uint32_t s_free = s_full + 16, pv_done = s_free + 16, p_full = pv_done + 16, o_done = p_full + 8;
+  const uint32_t q_ready = o_done + 8, drain = q_ready + 8, staged = drain + 8, unstaged = staged + 8 * L::kSlots;
   volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
   volatile int *bad_tag = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < 8; ++i) bad_tag[i] = 0;
+    for (int i = 0; i < 16; ++i) bad_tag[i] = 0;   // the loads are up to 8 tiles ahead of the softmax
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(kv_full + 8 * i, kConv * 32);
       mbar_init(kv_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, kSoft * 32);
+      mbar_init(s_free + 8 * i, kSoft * 32);
+      mbar_init(pv_done + 8 * i, 1);
     }
-    mbar_init(pv_done, 1);
+    mbar_init(p_full, kSoft * 32);
     mbar_init(o_done, 1);
     mbar_init(q_ready, kSoft * 32);
     mbar_init(drain, 1);
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(staged + 8 * i, 1);
+      mbar_init(unstaged + 8 * i, kConv);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == W_MMA_P) {
@@ -391,170 +461,220 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRestRegs));
     if (warp == W_MMA_P) {
     // ================================================================ MMA issuer
-    // Buffers in the order of use: K of the first tile, then per tile i the K
-    // of tile i + 1 (if any) and the V of tile i.
+    // Tiles in the order of use: K of the first kSBufs, then per tile i the K of
+    // tile i + kSBufs (if any) and the V of tile i.
     Walk walk(P);
     Segment G = {};
     uint32_t buf = 0, tile = 0, item = 0;
     bool ok = true;
-    auto qk = [&](uint32_t t) -> bool {             // S of tile t (global count) from the next buffer
-      const uint32_t x = buf % kBufs;
-      if (!mbar_wait_warp(kv_full + 8 * x, (buf / kBufs) & 1, abort_flag, A.dev_status)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t at = sbase + x * L::kTile;
+    auto qk = [&](uint32_t t) -> bool {             // S of tile t (counted over the CTA)
+      const uint32_t sb = t % L::kSBufs;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ts(tmem + L::kS + (t & 1) * T, tmem + L::kQ + 8 * k,
-                 gemm::desc_sw128(at + (k >> 2) * (T * 128)) + 2 * (k & 3), idesc(T, false), k > 0);
-        tc_commit(kv_empty + 8 * x);
-        tc_commit(s_full + 8 * (t & 1));
+      for (int u = 0; u < L::kUnits; ++u, ++buf) {
+        const uint32_t x = buf % kBufs;
+        if (!mbar_wait_warp(kv_full + 8 * x, (buf / kBufs) & 1, abort_flag, A.dev_status)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t at = sbase + x * L::kUnit;
+          constexpr int kSteps = D / 16 / L::kUnits;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            mma_ts(tmem + L::kS + sb * T, tmem + L::kQ + 8 * (u * kSteps + k),
+                   gemm::desc_sw128(at + (k >> 2) * (T * 128)) + 2 * (k & 3), idesc(T, false), u > 0 || k > 0);
+          tc_commit(kv_empty + 8 * x);
+          if (u + 1 == L::kUnits) tc_commit(s_full + 8 * sb);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      ++buf;
       return true;
     };
     while (ok && walk.next(P, G)) {
       if (!mbar_wait_warp(q_ready, item & 1, abort_flag, A.dev_status)) { ok = false; break; }
       tc_fence_after();
       const int n = G.s1 - G.s0;
-      if (!qk(tile)) { ok = false; break; }
-      for (int i = 0; i < n; ++i, ++tile) {
-        if (i + 1 < n) {
-          // S buffer (tile + 1) & 1 held P of tile - 1: wait until that was read
-          if (i > 0 && !mbar_wait_warp(pv_done, (tile - 1) & 1, abort_flag, A.dev_status)) { ok = false; break; }
-          if (!qk(tile + 1)) { ok = false; break; }
+      for (int i = 0; ok && i < L::kSBufs && i < n; ++i) ok = qk(tile + i);
+      for (int i = 0; ok && i < n; ++i, ++tile) {
+        if (i + L::kSBufs < n) {
+          const uint32_t sb = tile % L::kSBufs;
+          if (!mbar_wait_warp(s_free + 8 * sb, (tile / L::kSBufs) & 1, abort_flag, A.dev_status) ||
+              !qk(tile + L::kSBufs)) {
+            ok = false;
+            break;
+          }
         }
-        if (!mbar_wait_warp(p_full + 8 * (tile & 1), (tile >> 1) & 1, abort_flag, A.dev_status)) { ok = false; break; }
-        const uint32_t x = buf % kBufs;
-        if (!mbar_wait_warp(kv_full + 8 * x, (buf / kBufs) & 1, abort_flag, A.dev_status)) { ok = false; break; }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t at = sbase + x * L::kTile;
+        if (!mbar_wait_warp(p_full, tile & 1, abort_flag, A.dev_status)) { ok = false; break; }
 #pragma unroll
-          for (int k = 0; k < T / 16; ++k)
-            mma_ts(tmem + L::kO, tmem + L::kS + (tile & 1) * T + p_col<T>(k), desc_n_major(at + k * 2048, T * 128),
-                   idesc(D, true), i > 0 || k > 0);
-          tc_commit(kv_empty + 8 * x);
-          tc_commit(pv_done);
-          if (i + 1 == n) tc_commit(o_done);
+        for (int u = 0; ok && u < L::kUnits; ++u, ++buf) {
+          const uint32_t x = buf % kBufs;
+          if (!mbar_wait_warp(kv_full + 8 * x, (buf / kBufs) & 1, abort_flag, A.dev_status)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t at = sbase + x * L::kUnit;
+            constexpr int kKeys = T / L::kUnits;          // keys of a unit of V
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k) {
+              if (L::kPShared)
+                mma_ss(tmem + L::kO, gemm::desc_sw128(sbase + L::kPAt + u * (kRows * 128)) + 2 * k,
+                       desc_n_major(at + k * 2048, kKeys * 128), idesc(D, true), i > 0 || u > 0 || k > 0);
+              else
+                mma_ts(tmem + L::kO, tmem + L::kP + 8 * k, desc_n_major(at + k * 2048, kKeys * 128), idesc(D, true),
+                       i > 0 || k > 0);
+            }
+            tc_commit(kv_empty + 8 * x);
+            if (u + 1 == L::kUnits) {
+              tc_commit(pv_done + 8 * (tile & 1));
+              if (i + 1 == n) tc_commit(o_done);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        ++buf;
       }
       ++item;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       tc_commit(drain);
       const long long t0 = clock64();
       while (!gemm::mbar_try_wait(drain, 0) && clock64() - t0 < gemm::kWaitBudgetCycles) {}
     }
     __syncwarp();
-    }
-  } else if (warp >= W_CONV) {
-    // ================================================================ converters
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvRegs));
+    } else if (warp == W_LOAD) {
+    // ================================================================ loader
+    // Codes and scales of tiles in the order of use, a slot each.  Lane i copies
+    // the i-th `chunk` tokens of the tile, which lie on one page.  Tokens behind
+    // the sequence's end and on bad pages are not copied: what the slot holds in
+    // their place decodes to finite values, and their scores are masked.
     Walk walk(P);
     Segment G = {};
-    // A warp takes 16 tokens (8 with D = 256) of a tile, all on one page; a lane
-    // kPer neighbouring 16-byte pieces of one token.
-    constexpr int kPer = D == 64 ? 1 : 2;
-    constexpr int kTok = T / kConv;                       // tokens per warp
-    const int w = __shfl_sync(0xffffffffu, warp - W_CONV, 0);
-    const int t_lane = lane % kTok, p_lane = (lane / kTok) * kPer;
-    const int t = w * kTok + t_lane;
-    uint8_t *const dst = smem + (p_lane >> 1) * (T * 128) + t * 128;
-    const int lane_q = t_lane * (D / 2) + p_lane * 16, lane_s = t_lane * (D / 16) + p_lane * 2;
-    uint32_t buf = 0, tile = 0;
+    uint32_t load = 0, tile = 0;
     bool ok = true;
-    struct Piece { uint32_t code[4 * kPer], scale; };
-    Piece next_k, next_v;                                 // loaded, not yet converted
-    int32_t page = -1;                                    // page of the tile whose rows are next
-    int64_t row = -1, row_prev = -1;                      // pool row of that tile's first token, and of the one before
-    auto fetch_page = [&](int i) {                        // i: tile of the sequence
-      const int tok = i * T + w * kTok;
-      page = -1;
-      if (i < G.s1 && tok < G.seq.len)
-        page = __ldg(A.table + (int64_t)G.b * A.max_pages + fast_div((uint32_t)tok, A.by_page));
+    const int chunk = P.chunk, chunks = T / chunk;
+    auto fetch = [&](int i) -> int32_t {                  // this lane's page of tile i of the segment, -1 none, -2 bad
+      const int tok = (G.s0 + i) * T + lane * chunk;
+      if (lane >= chunks || G.s0 + i >= G.s1 || tok >= G.seq.len) return -1;
+      const int32_t page = __ldg(A.table + (int64_t)G.b * A.max_pages + fast_div((uint32_t)tok, A.by_page));
+      return kv::page_ok(page, A.num_pages) ? page : -2;
     };
-    auto row_of = [&](int i, uint32_t tag) {
-      const int tok = i * T + w * kTok;
-      row_prev = row;
-      row = -1;
-      if (i < G.s1 && tok < G.seq.len) {
-        if (kv::page_ok(page, A.num_pages)) {
-          const int in_page = tok - (int)fast_div((uint32_t)tok, A.by_page) * A.page_size;
-          row = kv::pool_row(page, A.heads_kv, A.page_size, G.head, in_page);
-        } else {
-          report(A.dev_status, NVFP4_ERR_INDEX);
-          bad_tag[tag & 7] = (int)tag + 1;
-        }
-      }
-    };
-    // Tokens past the sequence's end on its last page come along: their codes
-    // are finite, whatever the memory held, and their scores are masked.
-    auto load = [&](Piece &x, const uint8_t *q, const uint8_t *sf, int64_t at) {
-      if (at >= 0) {
-        const uint8_t *c = q + at * (D / 2) + lane_q, *s = sf + at * (D / 16) + lane_s;
-        if constexpr (kPer == 2) {
-          asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x.code[0]), "=r"(x.code[1]), "=r"(x.code[2]), "=r"(x.code[3]) : "l"(c));
-          asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x.code[4]), "=r"(x.code[5]), "=r"(x.code[6]), "=r"(x.code[7]) : "l"(c + 16));
-          x.scale = __ldg(reinterpret_cast<const uint32_t *>(s));
-        } else {
-          asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x.code[0]), "=r"(x.code[1]), "=r"(x.code[2]), "=r"(x.code[3]) : "l"(c));
-          x.scale = __ldg(reinterpret_cast<const uint16_t *>(s));
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4 * kPer; ++k) x.code[k] = 0;
-        x.scale = 0;
-      }
-    };
-    auto put = [&](const Piece &y) -> bool {              // convert into the next buffer
-      const uint32_t x = buf % kBufs;
-      if (buf >= kBufs && !mbar_wait_warp(kv_empty + 8 * x, ((buf / kBufs) - 1) & 1, abort_flag, A.dev_status))
+    auto copy = [&](int32_t page, int i, const uint8_t *q, const uint8_t *sf) -> bool {
+      const uint32_t slot = load % L::kSlots, bar = staged + 8 * slot, to = sbase + L::kStageAt + slot * L::kSlotBytes;
+      if (load >= L::kSlots &&
+          !mbar_wait_warp(unstaged + 8 * slot, ((load / L::kSlots) - 1) & 1, abort_flag, A.dev_status))
         return false;
-#pragma unroll
-      for (int p = 0; p < kPer; ++p) {
-        const uint32_t s0 = e4m3_pair_f16x2(__byte_perm(y.scale, 0, p ? 0x4242 : 0x4040));
-        const uint32_t s1 = e4m3_pair_f16x2(__byte_perm(y.scale, 0, p ? 0x4343 : 0x4141));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t s = k < 2 ? s0 : s1, c = y.code[4 * p + k];
-          const uint4 v = make_uint4(mul_f16x2(e2m1x2_f16x2<0>(c), s), mul_f16x2(e2m1x2_f16x2<1>(c), s),
-                                     mul_f16x2(e2m1x2_f16x2<2>(c), s), mul_f16x2(e2m1x2_f16x2<3>(c), s));
-          const int pos = (kPer == 2 ? p : p_lane & 1) * 4 + k;
-          *reinterpret_cast<uint4 *>(dst + x * L::kTile + ((pos ^ (t & 7)) << 4)) = v;
-        }
+      const uint32_t mine = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) {
+        if (mine) gemm::mbar_arrive_expect_tx(bar, __popc(mine) * chunk * (D / 2 + D / 16));
+        else mbar_arrive(bar);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(kv_full + 8 * x);
-      ++buf;
+      __syncwarp();
+      if (page >= 0) {
+        const int tok = (G.s0 + i) * T + lane * chunk;
+        const int in_page = tok - (int)fast_div((uint32_t)tok, A.by_page) * A.page_size;
+        const int64_t row = kv::pool_row(page, A.heads_kv, A.page_size, G.head, in_page);
+        gemm::bulk_load(to + lane * chunk * (D / 2), q + row * (D / 2), chunk * (D / 2), bar);
+        gemm::bulk_load(to + L::kCodeBytes + lane * chunk * (D / 16), sf + row * (D / 16), chunk * (D / 16), bar);
+      }
+      ++load;
       return true;
     };
     while (ok && walk.next(P, G)) {
       const int n = G.s1 - G.s0;
-      // K of tile 0; then K of tile 1 and V of tile 0 on their way, the page of tile 2
-      fetch_page(G.s0);
-      row_of(G.s0, tile);
-      load(next_k, A.k_q, A.k_sf, row);
-      fetch_page(G.s0 + 1);
-      if (!put(next_k)) break;
-      row_of(G.s0 + 1, tile + 1);
-      load(next_k, A.k_q, A.k_sf, row);
-      load(next_v, A.v_q, A.v_sf, row_prev);
-      fetch_page(G.s0 + 2);
-      for (int i = 0; i < n; ++i, ++tile) {
-        // K of tile i + 1, V of tile i; each register set is refilled for the next tile at once
-        if (i + 1 < n && !put(next_k)) { ok = false; break; }
-        row_of(G.s0 + i + 2, tile + 2);
-        load(next_k, A.k_q, A.k_sf, row);
-        fetch_page(G.s0 + i + 3);
-        if (!put(next_v)) { ok = false; break; }
-        load(next_v, A.v_q, A.v_sf, row_prev);
+      // K kSBufs tiles ahead of V; a tile's pages are read a step or more ahead
+      // of its K and kept until V's turn
+      constexpr int a = L::kSBufs;
+      int32_t p0 = fetch(0), p1 = fetch(1), p2 = a == 2 ? fetch(2) : -1;
+      for (int i = -a; ok && i < n; ++i) {
+        const int32_t p3 = i >= 0 ? fetch(i + a + 1) : -1;
+        const int k = i + a;
+        const int32_t pk = k == 0 ? p0 : a == 1 || k == 1 ? p1 : p2;
+        if (k < n) {
+          if (__any_sync(0xffffffffu, pk == -2)) {
+            if (pk == -2) report(A.dev_status, NVFP4_ERR_INDEX);
+            if (lane == 0) bad_tag[(tile + k) & 15] = (int)(tile + k) + 1;
+          }
+          ok = copy(pk, k, A.k_q, A.k_sf);
+        }
+        if (i >= 0) {
+          if (ok) ok = copy(p0, i, A.v_q, A.v_sf);
+          p0 = p1;
+          if (a == 2) { p1 = p2; p2 = p3; }
+          else p1 = p3;
+        }
+      }
+      tile += n;
+    }
+    // no copy is left on its way when the block ends
+    for (uint32_t x = load > L::kSlots ? load - L::kSlots : 0; x != load; ++x) {
+      const long long t0 = clock64();
+      while (!gemm::mbar_try_wait(staged + 8 * (x % L::kSlots), (x / L::kSlots) & 1) &&
+             clock64() - t0 < gemm::kWaitBudgetCycles) {}
+    }
+    }
+  } else if (warp >= W_CONV) {
+    // ================================================================ converters
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kConvRegs));
+    // A lane takes one 16-byte piece (32 codes) of one token of a unit.  Which
+    // piece depends on the token, so that 8 lanes read 8 different 16-byte
+    // positions of the staged rows (pairs of lanes share one in K with D = 256)
+    // and write 8 different ones of the swizzled tile.  With D = 64 a unit has
+    // work for half of the warps.
+    const int w = warp - W_CONV;
+    const bool idle = D == 64 && w >= kConv / 2;
+    int at_codes[2], at_scale[2], at_dst[2];              // of a unit of K, of V
+    uint32_t flips = 0;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int kTok = D == 64 ? 16 : D == 256 && v ? 4 : 8;
+      const int t = (w * kTok + lane % kTok) % T, c = lane / kTok;
+      const int p = D == 64 ? ((t >> 2) + c) & 1 : D == 256 && v ? (2 * t + c) & 7 : ((t >> 1) + c) & 3;
+      at_codes[v] = t * (D / 2) + p * 16;
+      at_scale[v] = L::kCodeBytes + t * (D / 16) + p * 2;
+      at_dst[v] = (p >> 1) * (T / (D == 256 && v ? 2 : 1) * 128) + t * 128;
+      flips |= (uint32_t)(((p & 1) * 4) ^ (t & 7)) << (8 * v);
+    }
+    Walk walk(P);
+    Segment G = {};
+    uint32_t buf = 0, load = 0;
+    bool ok = true;
+    while (ok && walk.next(P, G)) {
+      const int n = G.s1 - G.s0;
+      for (int j = 0; ok && j < 2 * n; ++j, ++load) {
+        // kSBufs tiles of K first, then K and V in turn, then the last V
+        const int first = min(L::kSBufs + 0, n);
+        const bool is_v = j >= first && (j >= 2 * n - first || ((j - first) & 1) != 0);
+        const uint32_t slot = load % L::kSlots;
+        if (!mbar_wait_warp(staged + 8 * slot, (load / L::kSlots) & 1, abort_flag, A.dev_status)) { ok = false; break; }
+#pragma unroll
+        for (int u = 0; ok && u < L::kUnits; ++u, ++buf) {
+          const uint32_t x = buf % kBufs;
+          // K: the unit's 128 elements of every token; V: its 64 tokens
+          const uint32_t from = sbase + L::kStageAt + slot * L::kSlotBytes;
+          const int code_u = u * (is_v ? 64 * (D / 2) : 64), scale_u = u * (is_v ? 64 * (D / 16) : 8);
+          const uint4 code = lds_v4(from + code_u + (is_v ? at_codes[1] : at_codes[0]));
+          const uint32_t scale = lds_u16(from + scale_u + (is_v ? at_scale[1] : at_scale[0]));
+          if (u + 1 == L::kUnits) {
+            __syncwarp();                                 // every lane has read the slot
+            if (lane == 0) mbar_arrive(unstaged + 8 * slot);
+          }
+          if (buf >= kBufs && !mbar_wait_warp(kv_empty + 8 * x, ((buf / kBufs) - 1) & 1, abort_flag, A.dev_status)) {
+            ok = false;
+            break;
+          }
+          if (!idle) {
+            const uint32_t s0 = e4m3_pair_f16x2(__byte_perm(scale, 0, 0x4040));
+            const uint32_t s1 = e4m3_pair_f16x2(__byte_perm(scale, 0, 0x4141));
+            const uint32_t c[4] = {code.x, code.y, code.z, code.w};
+            const uint32_t flip = (is_v ? flips >> 8 : flips) & 7;
+            uint8_t *dst = smem + x * L::kUnit + (is_v ? at_dst[1] : at_dst[0]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t s = k < 2 ? s0 : s1;
+              const uint4 v = make_uint4(mul_f16x2(e2m1x2_f16x2<0>(c[k]), s), mul_f16x2(e2m1x2_f16x2<1>(c[k]), s),
+                                         mul_f16x2(e2m1x2_f16x2<2>(c[k]), s), mul_f16x2(e2m1x2_f16x2<3>(c[k]), s));
+              *reinterpret_cast<uint4 *>(dst + ((flip ^ k) << 4)) = v;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(kv_full + 8 * x);
+        }
       }
     }
   } else {
@@ -562,7 +682,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
     Walk walk(P);
     Segment G = {};
-    constexpr int kHalf = T / 2;                          // keys of a tile per thread
     const int quad = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const int r = 32 * quad + lane;                       // row of the block
@@ -574,7 +693,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     bool ok = true;
     uint32_t qw[D / 4];                                   // this thread's half of its row of Q, bf16
     auto load_q = [&](const Segment &g) {
-      const int row = g.block * kRows + r, qi = row / A.group, h = g.head * A.group + row - qi * A.group;
+      const int row = g.block * kRows + r, qi = (int)fast_div((uint32_t)row, A.by_group), h = g.head * A.group + row - qi * A.group;
       if (r < g.nrows) {
         const uint16_t *q = A.q + (int64_t)(g.seq.first + qi) * A.ld_q + (int64_t)h * D + side * (D / 2);
 #pragma unroll
@@ -588,11 +707,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       }
     };
     bool more = walk.next(P, G);
-    if (more) load_q(G);
+    if (D <= 128 && more) load_q(G);
     while (more) {
+      if (D > 128) load_q(G);
       // ---- Q into tensor memory, each thread half of its row
       const bool live = r < G.nrows;
-      const int row = G.block * kRows + r, qi = row / A.group, h = G.head * A.group + row - qi * A.group;
+      const int row = G.block * kRows + r, qi = (int)fast_div((uint32_t)row, A.by_group), h = G.head * A.group + row - qi * A.group;
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) top = __vmaxu2(top, qw[i] & 0x7FFF7FFFu);
@@ -620,51 +740,44 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       float m = kFloor, l = 0.0f;
       const int n = G.s1 - G.s0;
       for (int i = 0; i < n; ++i, ++tile) {
-        const uint32_t x = tile & 1;
-        ok &= mbar_wait_warp(s_full + 8 * x, (tile >> 1) & 1, abort_flag, A.dev_status);
+        const uint32_t sb = tile % L::kSBufs;
+        ok &= mbar_wait_warp(s_full + 8 * sb, (tile / L::kSBufs) & 1, abort_flag, A.dev_status);
         tc_fence_after();
-        const uint32_t st = tmem + lanes + L::kS + x * T + side * kHalf;
-        uint32_t s[kHalf];
-        tm_ld<kHalf>(st, s);
-        const int tok0 = (G.s0 + i) * T + side * kHalf;
-        const int left = limit - tok0;                    // columns of this half that the row sees
-        const bool bad = bad_tag[tile & 7] == (int)tile + 1;
-        if (__any_sync(0xffffffffu, left < kHalf) || bad) {
-#pragma unroll
-          for (int k = 0; k < kHalf; ++k) s[k] = k < left ? s[k] : 0xFF800000u;
-          if (bad) {                                      // leave out the tokens of bad pages
-#pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-              if (tok0 + k < G.seq.len &&
-                  !kv::page_ok(__ldg(A.table + (int64_t)G.b * A.max_pages + fast_div((uint32_t)(tok0 + k), A.by_page)),
-                               A.num_pages))
-                s[k] = 0xFF800000u;
-          }
-        }
-        // ---- the row's largest score, over both halves
-        float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]), t2 = __uint_as_float(s[2]),
-              t3 = __uint_as_float(s[3]);
-#pragma unroll
-        for (int k = 4; k + 4 < kHalf; k += 8) {
-          t0 = max3(t0, __uint_as_float(s[k]), __uint_as_float(s[k + 4]));
-          t1 = max3(t1, __uint_as_float(s[k + 1]), __uint_as_float(s[k + 5]));
-          t2 = max3(t2, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 6]));
-          t3 = max3(t3, __uint_as_float(s[k + 3]), __uint_as_float(s[k + 7]));
-        }
-        t0 = max3(t0, __uint_as_float(s[kHalf - 4]), __uint_as_float(s[kHalf - 3]));
-        t1 = max3(t1, __uint_as_float(s[kHalf - 2]), __uint_as_float(s[kHalf - 1]));
-        float top_s = fmaxf(max3(t0, t1, t2), t3);
-        xch[(x * 2 + side) * kRows + r] = top_s;
+        uint32_t s[2][32];                                // this thread's 64 scores
+        tm_ld_begin(tmem + lanes + L::kS + sb * T + side * 64, s[0]);
+        tm_ld_begin(tmem + lanes + L::kS + sb * T + side * 64 + 32, s[1]);
+        tm_ld_end(s[0]);
+        tm_ld_end(s[1]);
+        tc_fence_before();
+        mbar_arrive(s_free + 8 * sb);
+        const int tok0 = (G.s0 + i) * T + side * 64;
+        const bool bad = bad_tag[tile & 15] == (int)tile + 1;
+        if (__any_sync(0xffffffffu, limit - tok0 < 64) || bad) mask_scores(A, G, s, limit - tok0, tok0, bad);
+        uint32_t p[32];
+        float sum = 0.0f;
+        if (i > 0) sum = weights(s, sc, m, p);
+        // Does the row's sum, over both threads, call for a larger maximum?  (A
+        // buffer of xch per tile parity: the last reads of one are a barrier back.)
+        volatile float *x = xch + (tile & 1) * 2 * kRows;
+        x[side * kRows + r] = sum;
         pair_sync(quad);
-        top_s = fmaxf(top_s, xch[(x * 2 + (side ^ 1)) * kRows + r]);
-        const float top_x = top_s == -INFINITY ? -INFINITY : top_s * sc;
-        if (__any_sync(0xffffffffu, top_x > m + kLazy)) { // the same decision in both warps of the rows
-          const float to = fmaxf(m, top_x);
+        const bool over = i == 0 || sum + x[(side ^ 1) * kRows + r] > kMostSum;
+        if (__any_sync(0xffffffffu, over)) {              // the same in both warps of the rows
+          float top = __uint_as_float(s[0][0]);
+#pragma unroll
+          for (int k = 1; k < 63; k += 2)
+            top = max3(top, __uint_as_float(s[k >> 5][k & 31]), __uint_as_float(s[(k + 1) >> 5][(k + 1) & 31]));
+          top = fmaxf(top, __uint_as_float(s[1][31]));
+          pair_sync(quad);                                // both have read the sums
+          x[side * kRows + r] = top;
+          pair_sync(quad);
+          top = fmaxf(top, x[(side ^ 1) * kRows + r]);
+          const float to = over ? fmaxf(m, top == -INFINITY ? -INFINITY : top * sc) : m;
           const float f = ex2(m - to);
           m = to;
           l *= f;
-          if (i > 0) {
-            ok &= mbar_wait_warp(pv_done, (tile - 1) & 1, abort_flag, A.dev_status);
+          if (i > 0) {                                    // O by the new maximum, half of the row each
+            ok &= mbar_wait_warp(pv_done + 8 * ((tile - 1) & 1), ((tile - 1) >> 1) & 1, abort_flag, A.dev_status);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -674,43 +787,46 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
               tm_st16(tmem + lanes + L::kO + side * (D / 2) + 16 * c, o);
             }
+            tm_wait_st();
           }
+          sum = weights(s, sc, m, p);
         }
-        // ---- P over this half of S
-        const uint64_t sc2 = pair_f32(sc, sc), neg_m = pair_f32(-m, -m);
-        uint64_t sum0 = 0, sum1 = 0;
-        uint32_t p[kHalf / 2];
+        l += sum;
+        // ---- P for the MMA, once P V of the tile before is over.  (Two barriers
+        // in turn: of the one waited for, every earlier phase is over, since S of
+        // this tile was committed behind the P V of three tiles back.)
+        if (tile > 0)
+          ok &= mbar_wait_warp(pv_done + 8 * ((tile - 1) & 1), ((tile - 1) >> 1) & 1, abort_flag, A.dev_status);
+        if (L::kPShared) {
+          uint8_t *at = smem + L::kPAt + side * (kRows * 128) + r * 128;
 #pragma unroll
-        for (int k = 0; k < kHalf / 2; ++k) {
-          const uint64_t v = fma_f32x2(((uint64_t)s[2 * k + 1] << 32) | s[2 * k], sc2, neg_m);
-          const float a = ex2(__uint_as_float((uint32_t)v)), b = ex2(__uint_as_float((uint32_t)(v >> 32)));
-          if (k & 1) sum1 = add_f32x2(sum1, pair_f32(a, b));
-          else sum0 = add_f32x2(sum0, pair_f32(a, b));
-          p[k] = pack_f16x2(a, b);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(at + ((k ^ (r & 7)) << 4)) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else {
+          tc_fence_after();
+          tm_st32(tmem + lanes + L::kP + side * 32, p);
+          tm_wait_st();
         }
-        sum0 = add_f32x2(sum0, sum1);
-        l += __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
-        tm_st<kHalf / 2>(st, p);
-        tm_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full + 8 * x);
+        mbar_arrive(p_full);
       }
       // ---- the item's last P V, then O out, each thread half of its row; the
       // next item's Q is on its way meanwhile
-      const Segment done = G;
+      const bool whole = G.s0 == 0 && G.s1 == G.steps;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + kv::part_slot(blockIdx.x, walk.per, G.item_start);
+      const int64_t at = (int64_t)(G.seq.first + qi) * A.heads_q + h;
       more = walk.next(P, G);
-      if (more) load_q(G);
+      if (D <= 128 && more) load_q(G);                    // (with D = 256 O and Q do not fit the registers at once)
       ok &= mbar_wait_warp(o_done, item & 1, abort_flag, A.dev_status);
       ++item;
       tc_fence_after();
-      pair_sync(quad);                                    // the other half's last read of xch is over
+      // the row's sum (the maximum is the same in both threads)
+      pair_sync(quad);
       xch[side * kRows + r] = l;
       pair_sync(quad);
-      l = xch[r] + xch[kRows + r];                        // both threads in the same order
+      l = xch[r] + xch[kRows + r];
       pair_sync(quad);
-      const bool whole = done.s0 == 0 && done.s1 == done.steps;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + kv::part_slot(blockIdx.x, walk.per, done.item_start);
-      const int64_t at = (int64_t)(done.seq.first + qi) * A.heads_q + h;
       const float f = whole ? (l == 0.0f ? 0.0f : vgs * kScaleFix / l) : 1.0f;
 #pragma unroll 1
       for (int c = side * (D / 64); c < (side + 1) * (D / 64); ++c) {
@@ -794,7 +910,7 @@ __global__ void __launch_bounds__(256) join_kernel(const PlanArgs P) {
       sum += f * ml.y;
       acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
     }
-    const int row = what.y * kRows + r, qi = row / A.group, h = head * A.group + row - qi * A.group;
+    const int row = what.y * kRows + r, qi = (int)fast_div((uint32_t)row, A.by_group), h = head * A.group + row - qi * A.group;
     const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
     const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
     store_out(A, at, D, d, acc, f);
@@ -815,6 +931,8 @@ nvfp4_status run_prefill(PlanArgs p, uint8_t *ws, cudaStream_t stream) {
   if (!host::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), L::kBytes)) return NVFP4_ERR_CUDA;
   const int64_t entries = prefill_entries(p.a.batch, p.a.max_query, p.a.group);
   p.tile = L::T;
+  p.chunk = kv::kPageGranule;
+  while (p.chunk < L::T && p.a.page_size % (2 * p.chunk) == 0) p.chunk *= 2;
   p.grid = host::sm_count();
   p.count = reinterpret_cast<int32_t *>(ws);
   ws += 256;
