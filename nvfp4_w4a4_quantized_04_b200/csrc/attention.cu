@@ -26,9 +26,10 @@
 //    turns into the second one's B operand by an 8x8 transpose (movmatrix).
 //  * Every warp has its own ring of cp.async stages (32 tokens of K and V) and
 //    its own softmax state; warps meet only at the end of an item.
-//  * The running maximum is raised only when a score exceeds it by more than
-//    2^8 (P stays below f16's range), so the usual step has one vote instead
-//    of a reduction and a rescale.
+//  * The weights are taken by the running maximum as it stands, which is raised
+//    only when a lane's weights of a step add up to more than 2^13 (P stays
+//    below f16's range): the usual step has one vote instead of a maximum, a
+//    reduction and a rescale.
 // Q is brought to f16 by a power of two per row that puts the row's largest
 // element at 2^14: exact for every element within 2^29 of it.
 //
@@ -47,10 +48,10 @@
 namespace nvfp4 {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                // tokens per step
-constexpr int kLeast = kWarps;           // fewest steps per CTA: one per warp
+// A step's weights of one lane may add up to this before the maximum is raised:
+// every weight then is an f16 (65504 is the largest).
+constexpr float kMostSum = 8192.0f;
 
 // ws_head: prefix[batch + 1], then steps per CTA.
 struct DecodeArgs {
@@ -106,7 +107,7 @@ __device__ __forceinline__ int v_piece(int t, int c) {
   return (pos ^ sw) * 16;
 }
 
-template <int D, int NT, int kStages>
+template <int D, int NT, int kStages, int kWarps>
 struct Layout {
   static constexpr int R = 8 * NT;
   static constexpr int kStageBytes = 2 * Half<D>::kBytes;
@@ -122,9 +123,10 @@ struct Layout {
   static constexpr int bytes(int batch) { return kPrefix + 4 * (batch + 2); }
 };
 
-template <int D, int NT, int kStages, int kMinCtas>
-__global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const DecodeArgs P) {
-  using L = Layout<D, NT, kStages>;
+template <int D, int NT, int kStages, int kWarps, int kMinCtas>
+__global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const DecodeArgs P) {
+  using L = Layout<D, NT, kStages, kWarps>;
+  constexpr int kThreads = kWarps * 32;
   using H = Half<D>;
   constexpr int R = L::R;
   constexpr int J = D / 16;              // k-steps of S, m-tiles of O
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
     __syncthreads();
   }
   const int total = s_prefix[A.batch];
-  const int per_cta = (int)kv::steps_per_cta(total, gridDim.x, kLeast);
+  const int per_cta = (int)kv::steps_per_cta(total, gridDim.x, kWarps)     /* one step per warp at least */;
   if (blockIdx.x == 0) {
     for (int b = tid; b <= A.batch; b += kThreads) P.ws_head[b] = s_prefix[b];
     if (tid == 0) P.ws_head[A.batch + 1] = per_cta;
@@ -244,7 +246,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
         else
           *reinterpret_cast<uint32_t *>(dst) = pack_f16x2(v[i] * up, v[i + 1] * up);
       }
-      if (lane == 0) s_row[r] = make_float2(A.scale_log2 * kgs * kScaleFix * down, __int_as_float(limit));
+      // never 0, so that a masked score of -inf stays -inf
+      if (lane == 0)
+        s_row[r] = make_float2(fmaxf(A.scale_log2 * kgs * kScaleFix * down, 1.17549435e-38f), __int_as_float(limit));
     }
     __syncthreads();
     float sc[NT][2];
@@ -257,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
         sc[nt][i] = x.x;
         lim[nt][i] = __float_as_int(x.y);
       }
+    // what every row sees (the rows that pad the block see nothing: they count as the first row)
+    const int lim_min = (int)kv::visible_keys(seq.len, seq.queries, 0, A.causal != 0);
 
     float o[J][NT][4];
 #pragma unroll
@@ -267,7 +273,13 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
         for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.0f;
     float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kFloor, l[nt][0] = l[nt][1] = 0.0f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // rows that pad the block (zeros, never stored) start where they stay
+        m[nt][i] = 8 * nt + 2 * t4 + i < nrows ? (float)kFloor : 0.0f;
+        l[nt][i] = 0.0f;
+      }
 
     // ---- the warp's steps: s0 + warp, + kWarps, ...
     const int mine = max(0, (s1 - s0 - warp + kWarps - 1) / kWarps);
@@ -324,68 +336,102 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
       const uint32_t st = ring + stage * L::kStageBytes;
       const int tok0 = (s0 + warp + it * kWarps) * kStep;
 
-      // S^T: tokens g and g + 8 of each half against the rows 2 t4, 2 t4 + 1
+      // S^T: tokens g and g + 8 of each half against the rows 2 t4, 2 t4 + 1.
+      // Both halves side by side: each fragment of Q is read once, and their
+      // chains of MMAs are independent.
       float s[2][NT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t hb = st + h * H::kBytes;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[h][nt][k] = 0.0f;
-        constexpr int kPieces = D == 256 ? 2 : 1;
+      constexpr int kPieces = D == 256 ? 2 : 1, kWords = D == 64 ? 2 : 4;
 #pragma unroll
-        for (int pc = 0; pc < kPieces; ++pc) {
-          uint32_t ka[4], kb[4], sa, sb;
+      for (int pc = 0; pc < kPieces; ++pc) {
+        uint32_t ka[2][4], kb[2][4], sa[2], sb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t hb = st + h * H::kBytes;
           if constexpr (D == 64) {
             const uint2 x = lds_v2(hb + H::kK + g * 32 + t4 * 8), y = lds_v2(hb + H::kK + (g + 8) * 32 + t4 * 8);
-            ka[0] = x.x; ka[1] = x.y; kb[0] = y.x; kb[1] = y.y;
-            sa = lds_u8(hb + H::kKs + g * 4 + t4);
-            sb = lds_u8(hb + H::kKs + (g + 8) * 4 + t4);
+            ka[h][0] = x.x; ka[h][1] = x.y; kb[h][0] = y.x; kb[h][1] = y.y;
+            sa[h] = lds_u8(hb + H::kKs + g * 4 + t4);
+            sb[h] = lds_u8(hb + H::kKs + (g + 8) * 4 + t4);
           } else {
             const uint4 x = lds_v4(hb + H::kK + k_piece<D>(g, t4 + 4 * pc));
             const uint4 y = lds_v4(hb + H::kK + k_piece<D>(g + 8, t4 + 4 * pc));
-            ka[0] = x.x; ka[1] = x.y; ka[2] = x.z; ka[3] = x.w;
-            kb[0] = y.x; kb[1] = y.y; kb[2] = y.z; kb[3] = y.w;
-            sa = lds_u16(hb + H::kKs + g * (D / 16) + 2 * (t4 + 4 * pc));
-            sb = lds_u16(hb + H::kKs + (g + 8) * (D / 16) + 2 * (t4 + 4 * pc));
+            ka[h][0] = x.x; ka[h][1] = x.y; ka[h][2] = x.z; ka[h][3] = x.w;
+            kb[h][0] = y.x; kb[h][1] = y.y; kb[h][2] = y.z; kb[h][3] = y.w;
+            sa[h] = lds_u16(hb + H::kKs + g * (D / 16) + 2 * (t4 + 4 * pc));
+            sb[h] = lds_u16(hb + H::kKs + (g + 8) * (D / 16) + 2 * (t4 + 4 * pc));
           }
-          constexpr int kWords = D == 64 ? 2 : 4;
+        }
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t fa = e4m3_pair_f16x2(__byte_perm(sa, 0, w < 2 ? 0x2020 : 0x2121));
-            const uint32_t fb = e4m3_pair_f16x2(__byte_perm(sb, 0, w < 2 ? 0x2020 : 0x2121));
-            const int j = pc * 8 + 2 * w;
-            const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(ka[w]), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(kb[w]), fb);
-            const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(ka[w]), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(kb[w]), fb);
-            const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(ka[w]), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(kb[w]), fb);
-            const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(ka[w]), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(kb[w]), fb);
+        for (int w = 0; w < kWords; ++w) {
+          const int j = pc * 8 + 2 * w;
+          uint2 q0[NT], q1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            q0[nt] = lds_v2(qs + (nt * J + j) * 256);
+            q1[nt] = lds_v2(qs + (nt * J + j + 1) * 256);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t fa = e4m3_pair_f16x2(__byte_perm(sa[h], 0, w < 2 ? 0x2020 : 0x2121));
+            const uint32_t fb = e4m3_pair_f16x2(__byte_perm(sb[h], 0, w < 2 ? 0x2020 : 0x2121));
+            const uint32_t a = ka[h][w], b = kb[h][w];
+            const uint32_t a0 = mul_f16x2(e2m1x2_f16x2<0>(a), fa), a1 = mul_f16x2(e2m1x2_f16x2<0>(b), fb);
+            const uint32_t a2 = mul_f16x2(e2m1x2_f16x2<1>(a), fa), a3 = mul_f16x2(e2m1x2_f16x2<1>(b), fb);
+            const uint32_t c0 = mul_f16x2(e2m1x2_f16x2<2>(a), fa), c1 = mul_f16x2(e2m1x2_f16x2<2>(b), fb);
+            const uint32_t c2 = mul_f16x2(e2m1x2_f16x2<3>(a), fa), c3 = mul_f16x2(e2m1x2_f16x2<3>(b), fb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q0 = lds_v2(qs + (nt * J + j) * 256), q1 = lds_v2(qs + (nt * J + j + 1) * 256);
-              mma_f16(s[h][nt], a0, a1, a2, a3, q0.x, q0.y);
-              mma_f16(s[h][nt], c0, c1, c2, c3, q1.x, q1.y);
+              mma_f16(s[h][nt], a0, a1, a2, a3, q0[nt].x, q0[nt].y);
+              mma_f16(s[h][nt], c0, c1, c2, c3, q1[nt].x, q1[nt].y);
             }
           }
         }
       }
 
-      // scores in log2 units, masked; does any exceed the running maximum by more than kLazy?
-      bool grow = false;
+      // The weights by the maximum as it stands; only when a lane's weights of
+      // this step add up to too much is the maximum raised and all of them taken
+      // again.  Steps that every row sees whole need no mask.
+      const bool all = tok0 + kStep <= lim_min && ((valid >> (2 * stage)) & 3) == 3;
+      if (!all) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool ok = (valid >> (2 * stage + h)) & 1;
-        const int t0 = tok0 + 16 * h + g;
+        for (int h = 0; h < 2; ++h) {
+          const bool ok = (valid >> (2 * stage + h)) & 1;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = s[h][nt][k] * sc[nt][k & 1];
-            s[h][nt][k] = (ok && t0 + (k >> 1) * 8 < lim[nt][k & 1]) ? x : -INFINITY;
-            grow |= s[h][nt][k] > m[nt][k & 1] + kLazy;
-          }
+            for (int k = 0; k < 4; ++k)
+              if (!ok || tok0 + 16 * h + g + (k >> 1) * 8 >= lim[nt][k & 1]) s[h][nt][k] = -INFINITY;
+        }
       }
-      if (__any_sync(0xffffffffu, grow)) {
+      uint32_t pb[2][NT][2];
+      float sum[NT][2];
+      auto take = [&]() {
+        float most = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[h][k] = ex2(fmaf(s[h][nt][k], sc[nt][k & 1], -m[nt][k & 1]));
+            pb[h][nt][0] = pack_f16x2(p[h][0], p[h][1]);
+            pb[h][nt][1] = pack_f16x2(p[h][2], p[h][3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            sum[nt][i] = (p[0][i] + p[0][i + 2]) + (p[1][i] + p[1][i + 2]);
+            most = fmaxf(most, sum[nt][i]);
+          }
+        }
+        return most;
+      };
+      if (__any_sync(0xffffffffu, take() > kMostSum)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -394,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[nt][i]);
+            x = fmaxf(x == -INFINITY ? x : x * sc[nt][i], m[nt][i]);
             const float f = ex2(m[nt][i] - x);
             m[nt][i] = x;
             l[nt][i] *= f;
@@ -404,21 +450,18 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
               o[j][nt][i + 2] *= f;
             }
           }
+        take();
       }
-      uint32_t pb[2][NT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] += sum[nt][0];
+        l[nt][1] += sum[nt][1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            p[k] = ex2(s[h][nt][k] - m[nt][k & 1]);
-            l[nt][k & 1] += p[k];
-          }
-          pb[h][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-          pb[h][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+        for (int h = 0; h < 2; ++h) {
+          pb[h][nt][0] = transpose8x8(pb[h][nt][0]);
+          pb[h][nt][1] = transpose8x8(pb[h][nt][1]);
         }
+      }
 
       // O^T += V^T P^T: lane (g, t4) holds head elements [g D/8, (g+1) D/8) of tokens 2 t4, 2 t4 + 1, + 8, + 9
 #pragma unroll
@@ -525,11 +568,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) decode_kernel(const Decode
 // Joins the parts of an item that several CTAs shared, and writes zeros for
 // the rows of sequences without keys.  One CTA per row of an item: kGroups
 // groups of D/4 threads take every kGroups-th part.
+constexpr int kJoin = 512;
 template <int D, int R>
-__global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P) {
-  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  __shared__ float4 s_o[256];
-  __shared__ float s_sum[kGroups], s_max[8];
+__global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
+  constexpr int kLanes = D / 4, kGroups = kJoin / kLanes;
+  __shared__ float4 s_o[kJoin];
+  __shared__ float s_sum[kGroups], s_max[kJoin / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Args &A = P.a;
   const int tid = threadIdx.x, lane = tid % kLanes, part = tid / kLanes;
@@ -549,7 +593,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P) {
     if (c0 == c1) return;
   }
   float M = kFloor, sum = 0.0f;
-  for (int c = c0 + tid; c <= c1; c += 256) {
+  for (int c = c0 + tid; c <= c1; c += kJoin) {
     const int slot = 2 * c + kv::part_slot(c, per, start);
     M = fmaxf(M, P.ws_ml[((int64_t)slot * R + r) * 2]);
   }
@@ -558,7 +602,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const DecodeArgs P) {
   if ((tid & 31) == 0) s_max[tid >> 5] = M;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) M = fmaxf(M, s_max[k]);
+  for (int k = 0; k < kJoin / 32; ++k) M = fmaxf(M, s_max[k]);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int c = c0 + part; c <= c1; c += kGroups) {
@@ -607,15 +651,16 @@ int64_t decode_workspace(int batch, int64_t rows, int D) {
   return align256(4 * ((int64_t)batch + 2)) + align256(2 * max_grid() * R * 8) + align256(2 * max_grid() * R * D * 4);
 }
 
-template <int D, int NT, int kStages, int kMinCtas>
+template <int D, int NT, int kStages, int kWarps, int kMinCtas>
 nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t stream) {
-  using L = Layout<D, NT, kStages>;
-  auto kern = decode_kernel<D, NT, kStages, kMinCtas>;
+  using L = Layout<D, NT, kStages, kWarps>;
+  constexpr int kThreads = kWarps * 32;
+  auto kern = decode_kernel<D, NT, kStages, kWarps, kMinCtas>;
   const int smem = L::bytes(p.a.batch);
   if (!host::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), L::bytes(kMaxBatch))) return NVFP4_ERR_CUDA;
   int64_t grid = (int64_t)host::sm_count() * host::blocks_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
   if (grid > max_grid()) grid = max_grid();
-  const int64_t want = (total_bound + kLeast - 1) / kLeast;
+  const int64_t want = (total_bound + kWarps - 1) / kWarps;
   if (grid > want) grid = want < 1 ? 1 : want;
   p.grid = (int32_t)grid;
   p.ws_head = reinterpret_cast<int32_t *>(ws);
@@ -627,7 +672,7 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.a.batch * p.a.heads_kv * L::R));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -725,17 +770,17 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   const int nt = tiles_for(rows, head_dim);
   const int64_t total_bound = (int64_t)batch * kv_heads * steps_max;
   if (head_dim == 64) {
-    if (nt == 1) return run<64, 1, 3, 4>(p, total_bound, ws, stream);
-    if (nt == 2) return run<64, 2, 3, 3>(p, total_bound, ws, stream);
-    return run<64, 4, 3, 2>(p, total_bound, ws, stream);
+    if (nt == 1) return run<64, 1, 3, 8, 2>(p, total_bound, ws, stream);
+    if (nt == 2) return run<64, 2, 3, 4, 3>(p, total_bound, ws, stream);
+    return run<64, 4, 3, 4, 2>(p, total_bound, ws, stream);
   }
   if (head_dim == 128) {
-    if (nt == 1) return run<128, 1, 3, 4>(p, total_bound, ws, stream);
-    if (nt == 2) return run<128, 2, 3, 3>(p, total_bound, ws, stream);
-    return run<128, 4, 3, 2>(p, total_bound, ws, stream);
+    if (nt == 1) return run<128, 1, 2, 8, 2>(p, total_bound, ws, stream);
+    if (nt == 2) return run<128, 2, 3, 4, 3>(p, total_bound, ws, stream);
+    return run<128, 4, 3, 4, 2>(p, total_bound, ws, stream);
   }
-  if (nt == 1) return run<256, 1, 2, 2>(p, total_bound, ws, stream);
-  return run<256, 2, 2, 2>(p, total_bound, ws, stream);
+  if (nt == 1) return run<256, 1, 2, 8, 1>(p, total_bound, ws, stream);
+  return run<256, 2, 2, 8, 1>(p, total_bound, ws, stream);
 }
 
 }  // extern "C"

@@ -92,6 +92,22 @@ __device__ __forceinline__ uint32_t bf16_of_sum(float hi, float lo) {
   return (uint32_t)__bfloat16_as_ushort(b);
 }
 
+// Packed pairs of fp32 (first in the low word).
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+// Two fp32 -> bf16x2, round to nearest even.
+__device__ __forceinline__ uint32_t bf16x2_of(uint64_t p) {
+  uint32_t d;
+  asm("{\n.reg .f32 l, h;\nmov.b64 {l, h}, %1;\ncvt.rn.bf16x2.f32 %0, h, l;\n}" : "=r"(d) : "l"(p));
+  return d;
+}
+
 // Per 16-element block: the block amax in integer SIMD, one IEEE division
 // for the scale and one IEEE reciprocal, the 16 products as eight packed
 // f32x2 multiplies, eight e2m1x2 conversions and one 8-byte store.

@@ -3,10 +3,12 @@
 // ("Qwen3.8-2.4T-A95B-NVFP4": NVFP4 KV cache, quantized when it is written).
 //
 // Rotation.  A pair (a, b) of a head becomes (a c - b s, b c + a s) with the
-// fp32 cosine and sine of the token's position; the products are formed with
-// their errors (fma) and the sum is rounded to bf16 once, so the result is the
-// correctly rounded one and the 4-bit codes behind it are reproducible.  The
-// block encode is the one of nvfp4_quantize with a given global scale.
+// fp32 cosine and sine of the token's position, rounded to bf16 once, so that
+// the 4-bit codes behind it are reproducible: from an interval that holds it,
+// or, where the interval's ends round apart, from the products with their errors
+// (fma).  The exact form alone, 25 instructions an element against 7, kept the
+// kernel from the memory rate.  The block encode is the one of nvfp4_quantize
+// with a given global scale.
 //
 // Bound by HBM: 2 bytes in and 9/16 out per element of k and v, 2 + 2 per
 // element of q.  A thread owns 32 elements of one token: the two 16-element
@@ -55,25 +57,59 @@ __device__ __forceinline__ uint32_t rot_bf16(float a, float c, float b, float s)
   return bf16_of_sum(hi, __fadd_rn(t, __fsub_rn(e, f)));
 }
 
+// The same for the usual element: q = b s and r = fma(a, c, -q) are off by less
+// than 2^-23 (|q| + |r|); where both ends of a wider interval round to the same
+// bf16 (all but about one element in 2^12), `lo` and `hi` agree.
+__device__ __forceinline__ void rot_interval(float a, float c, float b, float s, float &lo, float &hi) {
+  const float q = __fmul_rn(b, s), r = __fmaf_rn(a, c, -q);
+  const float e = fabsf(q) + fabsf(r);
+  lo = __fmaf_rn(e, -0x1p-22f, r);
+  hi = __fmaf_rn(e, 0x1p-22f, r);
+}
+
 // Rotate the two blocks x[0..7], x[8..15] (bf16 pairs).  Halves: element i of
 // the first block with element i of the second.  Pairs: neighbours.
 template <bool kPairs>
 __device__ __forceinline__ void rotate(uint32_t (&x)[16], const float (&c)[16], const float (&s)[16]) {
-  if constexpr (kPairs) {
+  uint32_t y[16], differ = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = half_f32(x[i], 0), b = half_f32(x[i], 1);
-      x[i] = rot_bf16(a, c[i], b, s[i]) | (rot_bf16(b, c[i], -a, s[i]) << 16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a0 = half_f32(x[i], 0), a1 = half_f32(x[i], 1);
-      const float b0 = half_f32(x[8 + i], 0), b1 = half_f32(x[8 + i], 1);
-      x[i] = rot_bf16(a0, c[2 * i], b0, s[2 * i]) | (rot_bf16(a1, c[2 * i + 1], b1, s[2 * i + 1]) << 16);
-      x[8 + i] = rot_bf16(b0, c[2 * i], -a0, s[2 * i]) | (rot_bf16(b1, c[2 * i + 1], -a1, s[2 * i + 1]) << 16);
+  for (int i = 0; i < (kPairs ? 16 : 8); ++i) {
+    // the word pairs (a0, a1), (b0, b1) become words ya, yb
+    float a0, a1, b0, b1, c0, c1, s0, s1, l[4], h[4];
+    if (kPairs) {
+      a0 = half_f32(x[i], 0); b0 = half_f32(x[i], 1); c0 = c[i]; s0 = s[i];
+      rot_interval(a0, c0, b0, s0, l[0], h[0]);
+      rot_interval(b0, c0, -a0, s0, l[1], h[1]);
+      y[i] = bf16x2_of(pair_f32(l[0], l[1]));
+      differ |= y[i] ^ bf16x2_of(pair_f32(h[0], h[1]));
+    } else {
+      a0 = half_f32(x[i], 0); a1 = half_f32(x[i], 1); b0 = half_f32(x[8 + i], 0); b1 = half_f32(x[8 + i], 1);
+      c0 = c[2 * i]; c1 = c[2 * i + 1]; s0 = s[2 * i]; s1 = s[2 * i + 1];
+      rot_interval(a0, c0, b0, s0, l[0], h[0]);
+      rot_interval(a1, c1, b1, s1, l[1], h[1]);
+      rot_interval(b0, c0, -a0, s0, l[2], h[2]);
+      rot_interval(b1, c1, -a1, s1, l[3], h[3]);
+      y[i] = bf16x2_of(pair_f32(l[0], l[1]));
+      y[8 + i] = bf16x2_of(pair_f32(l[2], l[3]));
+      differ |= (y[i] ^ bf16x2_of(pair_f32(h[0], h[1]))) | (y[8 + i] ^ bf16x2_of(pair_f32(h[2], h[3])));
     }
   }
+  if (differ) {
+#pragma unroll
+    for (int i = 0; i < (kPairs ? 16 : 8); ++i) {
+      if (kPairs) {
+        const float a = half_f32(x[i], 0), b = half_f32(x[i], 1);
+        y[i] = rot_bf16(a, c[i], b, s[i]) | (rot_bf16(b, c[i], -a, s[i]) << 16);
+      } else {
+        const float a0 = half_f32(x[i], 0), a1 = half_f32(x[i], 1);
+        const float b0 = half_f32(x[8 + i], 0), b1 = half_f32(x[8 + i], 1);
+        y[i] = rot_bf16(a0, c[2 * i], b0, s[2 * i]) | (rot_bf16(a1, c[2 * i + 1], b1, s[2 * i + 1]) << 16);
+        y[8 + i] = rot_bf16(b0, c[2 * i], -a0, s[2 * i]) | (rot_bf16(b1, c[2 * i + 1], -a1, s[2 * i + 1]) << 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = y[i];
 }
 
 __device__ __forceinline__ void load2(const uint16_t *p, int b0, int b1, bool v8, uint32_t (&x)[16]) {
@@ -90,26 +126,34 @@ __device__ __forceinline__ void load2(const uint16_t *p, int b0, int b1, bool v8
 __device__ __forceinline__ void put(const uint32_t (&x)[16], int b0, int b1, float gs, uint8_t *q, uint8_t *sf,
                                     int64_t at, int D, int32_t *dev_status) {
   const float tg = __fmul_rn(6.0f, gs);
+  uint2 codes[2];
+  uint32_t S[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint4 a = make_uint4(x[8 * i], x[8 * i + 1], x[8 * i + 2], x[8 * i + 3]);
     const uint4 b = make_uint4(x[8 * i + 4], x[8 * i + 5], x[8 * i + 6], x[8 * i + 7]);
-    uint32_t S;
     bool bad = false;
-    uint2 codes = encode_block16(a, b, gs, tg, S, bad);
+    codes[i] = encode_block16(a, b, gs, tg, S[i], bad);
     if (bad) {
-      codes = make_uint2(0, 0);
-      S = 0;
+      codes[i] = make_uint2(0, 0);
+      S[i] = 0;
       report(dev_status, NVFP4_ERR_NONFINITE);
     }
-    const int j = i ? b1 : b0;
-    *reinterpret_cast<uint2 *>(q + at * (D >> 1) + 8 * j) = codes;
-    sf[at * (D >> 4) + j] = (uint8_t)S;
+  }
+  uint8_t *to = q + at * (D >> 1), *so = sf + at * (D >> 4);
+  if (b1 == b0 + 1) {
+    *reinterpret_cast<uint4 *>(to + 8 * b0) = make_uint4(codes[0].x, codes[0].y, codes[1].x, codes[1].y);
+    *reinterpret_cast<uint16_t *>(so + b0) = (uint16_t)(S[0] | S[1] << 8);
+  } else {
+    *reinterpret_cast<uint2 *>(to + 8 * b0) = codes[0];
+    *reinterpret_cast<uint2 *>(to + 8 * b1) = codes[1];
+    so[b0] = (uint8_t)S[0];
+    so[b1] = (uint8_t)S[1];
   }
 }
 
 template <bool kPairs>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(128, 3) append_kernel(const AppendArgs A) {
   const int units = A.D >> 5;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (int64_t)A.tokens * units) return;
@@ -151,25 +195,30 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs A) {
     if (i == 0 && blockIdx.y == gridDim.y - 1 && (!(kg > 0.0f) || !isfinite(kg) || !(vg > 0.0f) || !isfinite(vg)))
       report(A.dev_status, NVFP4_ERR_INVALID_ARG);
   }
-  for (int h = h0; h < h1; ++h) {
+  // without a slot only the query heads are walked
+  const int end = keep ? h1 : min(h1, A.heads_q);
+  auto load_head = [&](int h, uint32_t (&x)[16]) {
+    if (h < A.heads_q) load2(A.q + token * A.ld_q + (int64_t)h * A.D, b0, b1, A.v8_q, x);
+    else if (h < A.heads_q + A.heads_kv) load2(A.k + token * A.ld_k + (int64_t)(h - A.heads_q) * A.D, b0, b1, A.v8_k, x);
+    else load2(A.v + token * A.ld_v + (int64_t)(h - A.heads_q - A.heads_kv) * A.D, b0, b1, A.v8_v, x);
+  };
+  uint32_t next[16];
+  if (h0 < end) load_head(h0, next);
+  for (int h = h0; h < end; ++h) {
     uint32_t x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = next[k];
+    if (h + 1 < end) load_head(h + 1, next);            // on its way while this head is turned and encoded
+    if (turn && h < A.heads_q + A.heads_kv) rotate<kPairs>(x, c, s);
     if (h < A.heads_q) {
-      load2(A.q + token * A.ld_q + (int64_t)h * A.D, b0, b1, A.v8_q, x);
-      if (turn) rotate<kPairs>(x, c, s);
       uint16_t *o = A.q_out + token * A.ld_qo + (int64_t)h * A.D;
       store_block(o + 16 * b0, A.v8_qo, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
       store_block(o + 16 * b1, A.v8_qo, make_uint4(x[8], x[9], x[10], x[11]), make_uint4(x[12], x[13], x[14], x[15]));
-    } else if (!keep) {
-      break;
     } else if (h < A.heads_q + A.heads_kv) {
-      const int hk = h - A.heads_q;
-      load2(A.k + token * A.ld_k + (int64_t)hk * A.D, b0, b1, A.v8_k, x);
-      if (turn) rotate<kPairs>(x, c, s);
-      put(x, b0, b1, kg, A.k_q, A.k_sf, pool_row(page, A.heads_kv, A.page_size, hk, row), A.D, A.dev_status);
+      put(x, b0, b1, kg, A.k_q, A.k_sf, pool_row(page, A.heads_kv, A.page_size, h - A.heads_q, row), A.D, A.dev_status);
     } else {
-      const int hv = h - A.heads_q - A.heads_kv;
-      load2(A.v + token * A.ld_v + (int64_t)hv * A.D, b0, b1, A.v8_v, x);
-      put(x, b0, b1, vg, A.v_q, A.v_sf, pool_row(page, A.heads_kv, A.page_size, hv, row), A.D, A.dev_status);
+      put(x, b0, b1, vg, A.v_q, A.v_sf, pool_row(page, A.heads_kv, A.page_size, h - A.heads_q - A.heads_kv, row), A.D,
+          A.dev_status);
     }
   }
 }
@@ -227,8 +276,8 @@ extern "C" nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void 
   int chunk = all < 16 ? all : 16;
   while (chunk > 1 && threads * ((all + chunk - 1) / chunk) < (int64_t)host::sm_count() * 1024) chunk = (chunk + 1) / 2;
   a.chunk = chunk;
-  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((all + chunk - 1) / chunk));
-  if (interleaved) append_kernel<true><<<grid, 256, 0, stream>>>(a);
-  else append_kernel<false><<<grid, 256, 0, stream>>>(a);
+  const dim3 grid((unsigned)((threads + 127) / 128), (unsigned)((all + chunk - 1) / chunk));
+  if (interleaved) append_kernel<true><<<grid, 128, 0, stream>>>(a);
+  else append_kernel<false><<<grid, 128, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

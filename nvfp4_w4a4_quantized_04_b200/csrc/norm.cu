@@ -16,8 +16,8 @@
 //
 // Rounding.  The sum of squares is kept in 64 bits (one conversion and one FMA
 // per element, which hide behind the loads) and 1/sqrt is one Newton step in 64 bits from the fp32 estimate (relative
-// error below 2^-40); y is formed as an unevaluated fp32 pair and rounded to
-// bf16 once.  So y is the correctly rounded value, and the codes behind it do
+// error below 2^-40); y is rounded to bf16 from an interval that holds it, or,
+// where the interval's ends round apart, from an unevaluated fp32 pair.  So y is the correctly rounded value, and the codes behind it do
 // not depend on the order of the sum.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,12 +39,6 @@ __device__ __forceinline__ uint4 pack4(const uint32_t *w) { return make_uint4(w[
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 // Two fp32 -> two E4M3 bytes (first in the low byte), round to nearest even,
 // saturating.
@@ -69,8 +63,9 @@ struct Args {
 enum { kFmtNone = 0, kFmtNvfp4 = 1, kFmtE4m3 = 2 };
 
 // kB blocks of 16 elements per thread; block index threadIdx.x + i * blockDim.x.
-template <int kFmt, bool kTiled, int kB>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const Args A) {
+// Up to kThreads threads, kCtas CTAs of that size per SM.
+template <int kFmt, bool kTiled, int kB, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) add_rmsnorm_kernel(const Args A) {
   __shared__ double s_sum[32];
   __shared__ uint32_t s_max[32];
   const int64_t row = blockIdx.x;
@@ -88,8 +83,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const Args A) {
         load_block_rw(A.res + row * A.ld_res + 16 * j, A.v8_res, c, d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t u = word(a, b, k), v = word(c, d, k);
-          r[i][k] = pack_bf16(__fadd_rn(lo_f32(u), lo_f32(v)), __fadd_rn(hi_f32(u), hi_f32(v)));
+          r[i][k] = bf16x2_of(add_f32x2(bf16x2_to_f32x2(word(a, b, k)), bf16x2_to_f32x2(word(c, d, k))));
         }
       } else {
 #pragma unroll
@@ -137,16 +131,31 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const Args A) {
       wa = __ldg(reinterpret_cast<const uint4 *>(A.w + 16 * j));
       wb = __ldg(reinterpret_cast<const uint4 *>(A.w + 16 * j + 8));
     }
+    // y = r w / sqrt(..): r * w is exact in fp32, and times the fp32 root it is off
+    // by less than 2^-23 of itself.  Where both ends of that interval round to
+    // the same bf16 -- for all but about one element in 2^12 -- that is y.
+    uint32_t yw[8], differ = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t w = word(wa, wb, k);
-      // r * w is exact in fp32; times hi + lo as p + (its error + t lo)
-      const float tl = __fmul_rn(lo_f32(r[i][k]), lo_f32(w)), th = __fmul_rn(hi_f32(r[i][k]), hi_f32(w));
-      const float pl = __fmul_rn(tl, rs_hi), ph = __fmul_rn(th, rs_hi);
-      const float el = __fmaf_rn(tl, rs_lo, __fmaf_rn(tl, rs_hi, -pl));
-      const float eh = __fmaf_rn(th, rs_lo, __fmaf_rn(th, rs_hi, -ph));
-      r[i][k] = bf16_of_sum(pl, el) | (bf16_of_sum(ph, eh) << 16);
+      const uint64_t t = mul_f32x2(bf16x2_to_f32x2(r[i][k]), bf16x2_to_f32x2(word(wa, wb, k)));
+      const uint64_t p = mul_f32x2(t, pair_f32(rs_hi, rs_hi));
+      yw[k] = bf16x2_of(mul_f32x2(p, pair_f32(1.0f - 0x1p-22f, 1.0f - 0x1p-22f)));
+      differ |= yw[k] ^ bf16x2_of(mul_f32x2(p, pair_f32(1.0f + 0x1p-22f, 1.0f + 0x1p-22f)));
     }
+    if (differ) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t w = word(wa, wb, k);
+        // times hi + lo as p + (its error + t lo)
+        const float tl = __fmul_rn(lo_f32(r[i][k]), lo_f32(w)), th = __fmul_rn(hi_f32(r[i][k]), hi_f32(w));
+        const float pl = __fmul_rn(tl, rs_hi), ph = __fmul_rn(th, rs_hi);
+        const float el = __fmaf_rn(tl, rs_lo, __fmaf_rn(tl, rs_hi, -pl));
+        const float eh = __fmaf_rn(th, rs_lo, __fmaf_rn(th, rs_hi, -ph));
+        yw[k] = bf16_of_sum(pl, el) | (bf16_of_sum(ph, eh) << 16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[i][k] = yw[k];
     const uint4 a = pack4(r[i]), b = pack4(r[i] + 4);
     if (A.y) store_block(A.y + row * (int64_t)A.K + 16 * j, A.v8_y, a, b);
     if constexpr (kFmt == kFmtNvfp4) {
@@ -188,9 +197,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const Args A) {
       uint32_t q[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t u = r[i][2 * k], v = r[i][2 * k + 1];
-        q[k] = e4m3x2(__fmul_rn(lo_f32(u), inv), __fmul_rn(hi_f32(u), inv)) |
-               (e4m3x2(__fmul_rn(lo_f32(v), inv), __fmul_rn(hi_f32(v), inv)) << 16);
+        const uint64_t u = mul_f32x2(bf16x2_to_f32x2(r[i][2 * k]), pair_f32(inv, inv));
+        const uint64_t v = mul_f32x2(bf16x2_to_f32x2(r[i][2 * k + 1]), pair_f32(inv, inv));
+        q[k] = e4m3x2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32))) |
+               (e4m3x2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))) << 16);
       }
       *reinterpret_cast<uint4 *>(A.q + row * (int64_t)A.K + 16 * j) = pack4(q);
     }
@@ -204,9 +214,10 @@ nvfp4_status launch(const Args &a, int64_t rows, cudaStream_t stream) {
   const int nblk = a.K >> 4;
   const int kb = nblk <= 1024 ? 1 : nblk <= 2048 ? 2 : 4;
   const int threads = ((nblk + kb - 1) / kb + 31) / 32 * 32;
-  if (kb == 1) add_rmsnorm_kernel<kFmt, kTiled, 1><<<(unsigned)rows, threads, 0, stream>>>(a);
-  else if (kb == 2) add_rmsnorm_kernel<kFmt, kTiled, 2><<<(unsigned)rows, threads, 0, stream>>>(a);
-  else add_rmsnorm_kernel<kFmt, kTiled, 4><<<(unsigned)rows, threads, 0, stream>>>(a);
+  if (kb == 1 && threads <= 384) add_rmsnorm_kernel<kFmt, kTiled, 1, 384, 4><<<(unsigned)rows, threads, 0, stream>>>(a);
+  else if (kb == 1) add_rmsnorm_kernel<kFmt, kTiled, 1, 1024, 1><<<(unsigned)rows, threads, 0, stream>>>(a);
+  else if (kb == 2) add_rmsnorm_kernel<kFmt, kTiled, 2, 1024, 1><<<(unsigned)rows, threads, 0, stream>>>(a);
+  else add_rmsnorm_kernel<kFmt, kTiled, 4, 1024, 1><<<(unsigned)rows, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 

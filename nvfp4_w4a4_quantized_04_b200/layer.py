@@ -8,6 +8,7 @@ the "Qwen3.8-Flash-Next-NVFP4" page, quantized W4A4).
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Optional
 
@@ -447,9 +448,22 @@ def _norm_args(x, weight, residual, residual_out):
 
 
 def _same_device(first, *others):
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """A context in which t's device is the current one (torch's own costs some
+    microseconds even when it already is)."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"CUDA tensors are wanted, not {t.device}")
+    return _HERE if torch._C._cuda_getDevice() == d else torch.cuda.device(d)
 
 
 def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch.Tensor, residual=None,
@@ -471,7 +485,7 @@ def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch
         raise ValueError("out: a packed tensor of this K and layout with enough rows is wanted")
     _same_device(x, global_scale, y, p.q)
     p.gs, p.offsets, p.num_groups, p.rows = global_scale, None, 1, rows
-    with torch.cuda.device(x.device):
+    with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
                                    NORM_NVFP4, global_scale, p.q, p.sf, layout, dev_status)
     return p, (residual_out if residual_out is not None else x), y
@@ -493,7 +507,7 @@ def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: 
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
         raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
     _same_device(x, q, scale, y)
-    with torch.cuda.device(x.device):
+    with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
                                    NORM_E4M3, scale, q, None, SF_ROWMAJOR, dev_status)
     return q, scale, (residual_out if residual_out is not None else x), y
@@ -576,7 +590,7 @@ class PagedKVCache:
             if q_out.shape != q.shape:
                 raise ValueError("q_out: the shape of q is wanted")
         _same_device(self.k_q, k, v, slots, q, q_out, positions, rope)
-        with torch.cuda.device(self.k_q.device):
+        with _on(self.k_q):
             nvfp4_kv_append(k, ld_k, v, ld_v, tokens, self.heads, D, slots, q, ld_q, hq, q_out, ld_qo, positions, rope,
                             rows, rot, int(interleaved), self.k_gs, self.v_gs, self.k_q, self.k_sf, self.v_q,
                             self.v_sf, self.num_pages, self.page_size, dev_status)
@@ -614,13 +628,14 @@ class PagedKVCache:
             raise ValueError(f"out: a contiguous {dt} tensor of q's shape is wanted")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous()):
             raise ValueError("lse: a contiguous fp32 [tokens, q_heads] tensor is wanted")
+        need = nvfp4_paged_attention_workspace_size(batch, max_query, hq, self.heads, D)
         if ws is None:
-            ws = self.workspace(batch, max_query, hq)
-        _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws)
-        if ws.numel() * ws.element_size() < nvfp4_paged_attention_workspace_size(batch, max_query, hq, self.heads, D):
+            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        elif ws.numel() * ws.element_size() < need:
             raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
+        _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws)
         scale = D ** -0.5 if softmax_scale is None else softmax_scale
-        with torch.cuda.device(self.k_q.device):
+        with _on(self.k_q):
             nvfp4_paged_attention(q, ld_q, tokens, query_offsets, max_query, seq_lens, batch, page_table,
                                   page_table.shape[1], hq, self.heads, D, self.k_q, self.k_sf, self.k_gs, self.v_q,
                                   self.v_sf, self.v_gs, self.num_pages, self.page_size, scale, int(causal), out,
@@ -632,7 +647,7 @@ class PagedKVCache:
         shape = (*self.k_q.shape[:3], self.head_dim)
         k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
         v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
-        with torch.cuda.device(self.k_q.device):
+        with _on(self.k_q):
             nvfp4_kv_dequantize(self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs,
                                 self.num_pages * self.page_size, self.heads, self.head_dim, k, v)
         return k, v
