@@ -183,6 +183,17 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     for (int b = tid; b <= A.batch; b += kThreads) P.ws_head[b] = s_prefix[b];
     if (tid == 0) P.ws_head[A.batch + 1] = per_cta;
   }
+  // sequences without keys: rows of zeros
+  for (int b = blockIdx.x; b < A.batch; b += gridDim.x) {
+    const Seq s = load_seq(A, b);
+    int steps;
+    if (!seq_steps(P, s, steps) || steps) continue;
+    for (int i = tid; i < s.queries * A.heads_q * (D / 4); i += kThreads) {
+      const int64_t at = (int64_t)s.first * A.heads_q + i / (D / 4);
+      store_out(A, at, D, (i % (D / 4)) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
+      if (A.lse && i % (D / 4) == 0) A.lse[at] = -INFINITY;
+    }
+  }
   const float kgs = __ldg(A.k_gs), vgs = __ldg(A.v_gs);
   int pos = (int)min((int64_t)total, (int64_t)blockIdx.x * per_cta);
   const int end = (int)min((int64_t)total, (int64_t)pos + per_cta);
@@ -565,9 +576,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
   }
 }
 
-// Joins the parts of an item that several CTAs shared, and writes zeros for
-// the rows of sequences without keys.  One CTA per row of an item: kGroups
-// groups of D/4 threads take every kGroups-th part.
+// Joins the items that several CTAs shared: CTA (c, r) row r of the item in
+// which CTA c's range of the first kernel begins, if it began earlier and c is
+// the first to continue it.  kGroups groups of D/4 threads take every kGroups-th
+// part.
 constexpr int kJoin = 512;
 template <int D, int R>
 __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
@@ -577,26 +589,21 @@ __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Args &A = P.a;
   const int tid = threadIdx.x, lane = tid % kLanes, part = tid / kLanes;
-  const int r = blockIdx.x % R;
-  const int idx = blockIdx.x / R;
-  const int head = idx % A.heads_kv, b = idx / A.heads_kv;
+  const int r = blockIdx.y, c = blockIdx.x + 1;
+  const int per = P.ws_head[A.batch + 1], total = P.ws_head[A.batch];
+  const int64_t pos = (int64_t)c * per;
+  if (per == 0 || pos >= total) return;  // refused offsets; or a CTA without work
+  const int b = upper_group(P.ws_head, A.batch, pos);
   const Seq seq = load_seq(A, b);
   int steps;
   if (!seq_steps(P, seq, steps) || r >= seq.queries * A.group) return;
-  const int per = P.ws_head[A.batch + 1];
-  if (per == 0) return;                  // refused offsets
+  const int head = ((int)pos - P.ws_head[b]) / steps;
   const int start = P.ws_head[b] + head * steps;
-  int c0 = 0, c1 = -1;
-  if (steps) {
-    c0 = start / per;
-    c1 = (start + steps - 1) / per;
-    if (c0 == c1) return;
-  }
+  if (start == pos || (int64_t)(c - 1) * per > start) return;
+  const int c0 = c - 1, c1 = (start + steps - 1) / per;
   float M = kFloor, sum = 0.0f;
-  for (int c = c0 + tid; c <= c1; c += kJoin) {
-    const int slot = 2 * c + kv::part_slot(c, per, start);
-    M = fmaxf(M, P.ws_ml[((int64_t)slot * R + r) * 2]);
-  }
+  for (int k = c0 + tid; k <= c1; k += kJoin)
+    M = fmaxf(M, P.ws_ml[((int64_t)(2 * k + kv::part_slot(k, per, start)) * R + r) * 2]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   if ((tid & 31) == 0) s_max[tid >> 5] = M;
@@ -605,8 +612,8 @@ __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
   for (int k = 0; k < kJoin / 32; ++k) M = fmaxf(M, s_max[k]);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int c = c0 + part; c <= c1; c += kGroups) {
-    const int64_t slot = (int64_t)(2 * c + kv::part_slot(c, per, start)) * R + r;
+  for (int k = c0 + part; k <= c1; k += kGroups) {
+    const int64_t slot = (int64_t)(2 * k + kv::part_slot(k, per, start)) * R + r;
     const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + slot * 2);
     const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + slot * D + lane * 4);
     const float f = ex2(ml.x - M);
@@ -628,8 +635,7 @@ __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
   const int qi = r / A.group, h = head * A.group + r - qi * A.group;
   const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
   const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
-  const int d = lane * 4;
-  store_out(A, at, D, d, acc, f);
+  store_out(A, at, D, lane * 4, acc, f);
   if (A.lse && lane == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
@@ -670,8 +676,9 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   p.ws_o = reinterpret_cast<float *>(ws);
   kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
+  if (grid == 1) return NVFP4_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.a.batch * p.a.heads_kv * L::R));
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)L::R);
   cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

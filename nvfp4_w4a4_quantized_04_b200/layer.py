@@ -419,9 +419,10 @@ class MoELayer:
 # ---------------------------------------------------------------- the norm in front of a projection
 def _rows(t: torch.Tensor, K: int, what: str):
     """A bf16 [rows, K] operand with unit stride along K: its row stride."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != K or (t.stride(1) != 1 and K > 1):
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(shape) != 2 or shape[1] != K or (stride[1] != 1 and K > 1):
         raise ValueError(f"{what}: a bf16 [rows, {K}] tensor with contiguous rows is wanted")
-    return t.stride(0) if t.shape[0] > 1 else K
+    return stride[0] if shape[0] > 1 else K
 
 
 def _norm_args(x, weight, residual, residual_out):
@@ -436,10 +437,10 @@ def _norm_args(x, weight, residual, residual_out):
         if residual.shape != x.shape:
             raise ValueError("residual: the shape of x is wanted")
         ld_res = _rows(residual, K, "residual")
-    if residual_out is None and residual is not None:
-        residual_out = torch.empty((rows, K), dtype=torch.bfloat16, device=x.device)
     ld_ro = 0
-    if residual_out is not None:
+    if residual_out is None and residual is not None:
+        residual_out, ld_ro = torch.empty_like(x, memory_format=torch.contiguous_format), K
+    elif residual_out is not None:
         if residual_out.shape != x.shape:
             raise ValueError("residual_out: the shape of x is wanted")
         ld_ro = _rows(residual_out, K, "residual_out")
@@ -497,12 +498,12 @@ def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: 
     scale fp32 [rows], r, y); q * scale[:, None] stands for y."""
     rows, K, ld_x, ld_res, residual_out, ld_ro = _norm_args(x, weight, residual, residual_out)
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
-    if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    if q.element_size() != 1 or q.shape != x.shape or not q.is_contiguous():
+        q = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+    elif q.element_size() != 1 or q.shape != x.shape or not q.is_contiguous():
         raise ValueError("q: a contiguous one-byte tensor of x's shape is wanted")
-    if scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous():
+    if scale is None:
+        scale = weight.new_empty(rows, dtype=torch.float32)
+    elif scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous():
         raise ValueError("scale: fp32 [rows] is wanted")
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
         raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
@@ -525,11 +526,12 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
 
 def _heads(t: torch.Tensor, tokens, D: int, what: str):
     """A bf16 [tokens, heads, D] operand whose heads of a token are contiguous: its token stride."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != D or (tokens is not None and t.shape[0] != tokens):
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != D or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{what}: a bf16 [tokens, heads, {D}] tensor is wanted")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != D):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return stride[0] if shape[0] > 1 else shape[1] * D
 
 
 class PagedKVCache:
@@ -553,6 +555,7 @@ class PagedKVCache:
                 raise ValueError(f"{name}: an fp32 tensor of one element is wanted")
         _same_device(k_q, k_sf, k_gs, v_q, v_sf, v_gs)
         self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs = k_q, k_sf, k_gs, v_q, v_sf, v_gs
+        self._need = {}                 # workspace bytes by (batch, max_query, q_heads)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, k_gs: torch.Tensor, v_gs: torch.Tensor,
@@ -585,10 +588,11 @@ class PagedKVCache:
         if q is not None:
             ld_q, hq = _heads(q, tokens, D, "q"), q.shape[1]
             if q_out is None:
-                q_out = torch.empty((tokens, hq, D), dtype=torch.bfloat16, device=q.device)
-            ld_qo = _heads(q_out, tokens, D, "q_out")
-            if q_out.shape != q.shape:
-                raise ValueError("q_out: the shape of q is wanted")
+                q_out, ld_qo = torch.empty_like(q, memory_format=torch.contiguous_format), hq * D
+            else:
+                ld_qo = _heads(q_out, tokens, D, "q_out")
+                if q_out.shape != q.shape:
+                    raise ValueError("q_out: the shape of q is wanted")
         _same_device(self.k_q, k, v, slots, q, q_out, positions, rope)
         with _on(self.k_q):
             nvfp4_kv_append(k, ld_k, v, ld_v, tokens, self.heads, D, slots, q, ld_q, hq, q_out, ld_qo, positions, rope,
@@ -611,7 +615,7 @@ class PagedKVCache:
         fp32 [tokens, q_heads] to fill.  Returns out [tokens, q_heads, D]."""
         D = self.head_dim
         ld_q = _heads(q, None, D, "q")
-        tokens, hq = q.shape[0], q.shape[1]
+        tokens, hq, _ = q.shape
         if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
             raise ValueError("seq_lens: a contiguous int32 [batch] tensor is wanted")
         batch = seq_lens.shape[0]
@@ -623,14 +627,17 @@ class PagedKVCache:
             raise ValueError("query_offsets: a contiguous int32 [batch + 1] tensor is wanted")
         dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
         if out is None:
-            out = torch.empty((tokens, hq, D), dtype=dt, device=q.device)
+            out = torch.empty_like(q, dtype=dt, memory_format=torch.contiguous_format)
         elif out.dtype != dt or out.shape != q.shape or not out.is_contiguous():
             raise ValueError(f"out: a contiguous {dt} tensor of q's shape is wanted")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, hq) or not lse.is_contiguous()):
             raise ValueError("lse: a contiguous fp32 [tokens, q_heads] tensor is wanted")
-        need = nvfp4_paged_attention_workspace_size(batch, max_query, hq, self.heads, D)
+        need = self._need.get((batch, max_query, hq))
+        if need is None:
+            need = self._need[batch, max_query, hq] = nvfp4_paged_attention_workspace_size(batch, max_query, hq,
+                                                                                           self.heads, D)
         if ws is None:
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+            ws = self.k_q.new_empty(max(need, 1))
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
         _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws)
@@ -645,8 +652,8 @@ class PagedKVCache:
     def dequantize(self):
         """The whole pool back in bf16: (k, v), each [num_pages, heads, page_size, D]."""
         shape = (*self.k_q.shape[:3], self.head_dim)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
-        v = torch.empty(shape, dtype=torch.bfloat16, device=self.k_q.device)
+        k = self.k_q.new_empty(shape, dtype=torch.bfloat16)
+        v = torch.empty_like(k)
         with _on(self.k_q):
             nvfp4_kv_dequantize(self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs,
                                 self.num_pages * self.page_size, self.heads, self.head_dim, k, v)
