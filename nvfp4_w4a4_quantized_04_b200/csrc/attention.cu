@@ -677,16 +677,8 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
   if (grid == 1) return NVFP4_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)L::R);
-  cfg.blockDim = dim3(kJoin);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, L::R>, p) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  return launch_behind(combine_kernel<D, L::R>, dim3((unsigned)(grid - 1), (unsigned)L::R), kJoin, 0, stream, p)
+             ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 }  // namespace attn
@@ -769,10 +761,14 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.row_cap = cap;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   if (rows > cap) {
-    // a single sequence has one form only; a batch may hold both kinds
+    // A batch may hold sequences for either form, each of which takes its own; a
+    // single one, or a batch of twice the decode form's rows on average, goes to
+    // the prefill form whole: the second pair of launches (about 12 us) costs more
+    // than few rows lose there.
+    const bool one_form = batch == 1 || tokens * group >= 2 * (int64_t)cap * batch;
     const nvfp4_status st =
-        launch_prefill(p.a, head_dim, batch == 1 ? 0 : cap, ws + decode_workspace(batch, rows, head_dim), stream);
-    if (st != NVFP4_OK || batch == 1) return st;
+        launch_prefill(p.a, head_dim, one_form ? 0 : cap, ws + decode_workspace(batch, rows, head_dim), stream);
+    if (st != NVFP4_OK || one_form) return st;
   }
   const int nt = tiles_for(rows, head_dim);
   const int64_t total_bound = (int64_t)batch * kv_heads * steps_max;

@@ -34,6 +34,23 @@ __device__ __forceinline__ void store_out(const Args &A, int64_t at, int D, int 
   }
 }
 
+// Launch that may be set up while the kernel before it on the stream still
+// runs; the kernel itself waits for it (griddepcontrol.wait) before it reads.
+template <typename Kernel, typename Params>
+inline bool launch_behind(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
+}
+
 inline int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Prefill form: sequences with more than row_floor rows.

@@ -145,6 +145,7 @@ __device__ __forceinline__ int block_scan(int v, int *scratch) {
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs P) {
   __shared__ int32_t first[kMaxBatch + 1];      // first entry of each sequence
   __shared__ int scratch[32], carry;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Args &A = P.a;
   const int t = threadIdx.x;
   bool bad = false;
@@ -456,6 +457,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  asm volatile("griddepcontrol.wait;" ::: "memory");         // the plan is written
 
   if (warp >= W_MMA_P) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRestRegs));
@@ -874,9 +876,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
 
 // Joins the items that several CTAs shared.  CTA (c, y): the item in which
 // CTA c's range of the prefill kernel begins, if c is the second CTA with tiles
-// of it; 16 rows of it.
+// of it; kJoinRows rows of it, one per D/4 threads.
+template <int D> constexpr int kJoinRows = 256 / (D / 4);
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const PlanArgs P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Args &A = P.a;
   const int per = P.count[1], total = P.count[2];
   const int c = blockIdx.x + 1;
@@ -893,29 +897,28 @@ __global__ void __launch_bounds__(256) join_kernel(const PlanArgs P) {
   if (c0 != c - 1) return;                      // not the second CTA
   const Seq seq = load_seq(A, what.x);
   const int nrows = min(kRows, seq.queries * A.group - what.y * kRows);
-  constexpr int kLanes = D / 4, kPass = 256 / kLanes;
-  const int d = (threadIdx.x % kLanes) * 4;
-  for (int i = threadIdx.x / kLanes; i < 16; i += kPass) {
-    const int r = blockIdx.y * 16 + i;
-    if (r >= nrows) return;
-    float M = kFloor, sum = 0.0f;
-    for (int k = c0; k <= c1; ++k)
-      M = fmaxf(M, P.ws_ml[((int64_t)(2 * k + kv::part_slot(k, per, start)) * kRows + r) * 2]);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = c0; k <= c1; ++k) {
-      const int64_t at = (int64_t)(2 * k + kv::part_slot(k, per, start)) * kRows + r;
-      const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + at * 2);
-      const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + at * D + d);
-      const float f = ex2(ml.x - M);
-      sum += f * ml.y;
-      acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-    }
-    const int row = what.y * kRows + r, qi = (int)fast_div((uint32_t)row, A.by_group), h = head * A.group + row - qi * A.group;
-    const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
-    const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
-    store_out(A, at, D, d, acc, f);
-    if (A.lse && d == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+  constexpr int kLanes = D / 4;
+  const int d = (threadIdx.x % kLanes) * 4, r = blockIdx.y * kJoinRows<D> + threadIdx.x / kLanes;
+  if (r >= nrows) return;
+  float M = kFloor, sum = 0.0f;
+  for (int k = c0; k <= c1; ++k)
+    M = fmaxf(M, P.ws_ml[((int64_t)(2 * k + kv::part_slot(k, per, start)) * kRows + r) * 2]);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = c0; k <= c1; ++k) {
+    const int64_t at = (int64_t)(2 * k + kv::part_slot(k, per, start)) * kRows + r;
+    const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + at * 2);
+    const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + at * D + d);
+    const float f = ex2(ml.x - M);
+    sum += f * ml.y;
+    acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
   }
+  const int row = what.y * kRows + r, qi = (int)fast_div((uint32_t)row, A.by_group),
+            h = head * A.group + row - qi * A.group;
+  const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
+  const float f = sum == 0.0f ? 0.0f : __ldg(A.v_gs) * kScaleFix / sum;
+  store_out(A, at, D, d, acc, f);
+  if (A.lse && d == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -947,10 +950,14 @@ nvfp4_status run_prefill(PlanArgs p, uint8_t *ws, cudaStream_t stream) {
   p.ws_o = reinterpret_cast<float *>(ws);
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
-  kern<<<(unsigned)p.grid, kPreThreads, L::kBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
-  if (p.grid > 1) join_kernel<D><<<dim3((unsigned)(p.grid - 1), kRows / 16), 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  // both may be set up while the kernel before them ends (griddepcontrol.wait)
+  if (!launch_behind(kern, dim3((unsigned)p.grid), kPreThreads, L::kBytes, stream, p)) return NVFP4_ERR_CUDA;
+  // an item takes at most all of a CTA's rows: rows beyond max_query * group do not exist
+  const int64_t rows = (int64_t)p.a.max_query * p.a.group < kRows ? (int64_t)p.a.max_query * p.a.group : kRows;
+  if (p.grid > 1 && !launch_behind(join_kernel<D>, dim3((unsigned)(p.grid - 1), (unsigned)((rows + kJoinRows<D> - 1) / kJoinRows<D>)),
+                                   256, 0, stream, p))
+    return NVFP4_ERR_CUDA;
+  return NVFP4_OK;
 }
 
 }  // namespace
