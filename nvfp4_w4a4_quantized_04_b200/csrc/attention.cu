@@ -756,6 +756,8 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.a.causal = causal;
   p.a.out = out;
   p.a.out_bf16 = out_dtype == NVFP4_OUT_BF16;
+  p.a.v8_q = aligned(q, 32) && ld_q % 16 == 0;
+  p.a.v8_out = aligned(out, 32);
   p.a.lse = lse;
   p.a.dev_status = dev_status;
   p.row_cap = cap;

@@ -29,6 +29,7 @@ struct Args {
   int32_t causal;
   void *out;                   // [tokens, q_heads, D]
   int32_t out_bf16;
+  bool v8_q, v8_out;           // rows of q, of a bf16 out begin on 32 bytes
   float *lse;                  // [tokens, q_heads] or null
   int32_t *dev_status;
 };

@@ -42,6 +42,7 @@
 // and items that several CTAs share are joined by a third kernel.
 #include "attention.cuh"
 #include "attention_internal.cuh"
+#include "encode.cuh"
 #include "gemm_common.cuh"
 #include "host_util.cuh"
 
@@ -79,9 +80,8 @@ template <int D> struct Pre {
   static constexpr int kUnit = T * D * 2 / kUnits;      // bytes of one
   static constexpr int kBufs = 4;                       // units in the ring
   static constexpr bool kPShared = D == 256;            // P in shared memory, else in tensor memory
-  static constexpr int kSBufs = D == 256 ? 1 : 2;       // S tiles in tensor memory
   static constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;   // tensor memory columns
-  static constexpr uint32_t kP = kS + kSBufs * T;       // (unless shared)
+  static constexpr uint32_t kP = kS + T;                // two P tiles in turn (unless shared)
   static constexpr uint32_t kCols = 512;
   static constexpr int kPAt = kBufs * kUnit;
   static constexpr int kPBytes = kPShared ? kRows * T * 2 : 0;
@@ -90,12 +90,12 @@ template <int D> struct Pre {
   static constexpr int kCodeBytes = T * D / 2, kScaleBytes = T * D / 16, kSlotBytes = kCodeBytes + kScaleBytes;
   static constexpr int kStageAt = kPAt + kPBytes;
   static constexpr int kBar = kStageAt + kSlots * kSlotBytes;
-  // kv_full[], kv_empty[], s_full[2], s_free[2], pv_done[2], p_full, o_done, q_ready, drain, staged[], unstaged[]
-  static constexpr int kNumBars = 2 * kBufs + 2 + 2 + 2 + 4 + 2 * kSlots;
+  // kv_full[], kv_empty[], s_full, s_free, pv_done, p_full, o_done, q_ready, drain, staged[], unstaged[]
+  static constexpr int kNumBars = 2 * kBufs + 7 + 2 * kSlots;
   static constexpr int kMisc = kBar + kNumBars * 8;      // tmem base, abort flag, bad-page tags[16]
   static constexpr int kXch = kMisc + 8 + 64;            // [4][128] floats between a row's two threads
   static constexpr int kBytes = kXch + 4 * kRows * 4 + 1024;
-  static_assert(kS + kSBufs * T + (kPShared ? 0 : T / 2) <= kCols, "tensor memory");
+  static_assert(kS + T + (kPShared ? 0 : T) <= kCols, "tensor memory");
   static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -334,18 +334,9 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t chunk) 
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Packed pairs of fp32 (first in the low word).
-__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
-  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -358,6 +349,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ void pair_sync(int quadrant) {
   asm volatile("bar.sync %0, 64;" :: "r"(1 + quadrant) : "memory");
 }
+// The same, and whether any of the 64 threads says so.
+__device__ __forceinline__ bool pair_any(int quadrant, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %2, 0;\nbar.red.or.pred p, %1, 64, q;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(any) : "r"(1 + quadrant), "r"((uint32_t)x) : "memory");
+  return any != 0;
+}
+
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
   const Args &A = P.a;
   const uint32_t sbase = smem_addr(smem);
   const uint32_t kv_full = sbase + L::kBar, kv_empty = kv_full + 8 * kBufs, s_full = kv_empty + 8 * kBufs;
-  const uint32_t s_free = s_full + 16, pv_done = s_free + 16, p_full = pv_done + 16, o_done = p_full + 8;
+  const uint32_t s_free = s_full + 8, pv_done = s_free + 8, p_full = pv_done + 8, o_done = p_full + 8;
   const uint32_t q_ready = o_done + 8, drain = q_ready + 8, staged = drain + 8, unstaged = staged + 8 * L::kSlots;
   volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -433,11 +433,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       mbar_init(kv_full + 8 * i, kConv * 32);
       mbar_init(kv_empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_free + 8 * i, kSoft * 32);
-      mbar_init(pv_done + 8 * i, 1);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, kSoft * 32);
+    mbar_init(pv_done, 1);
     mbar_init(p_full, kSoft * 32);
     mbar_init(o_done, 1);
     mbar_init(q_ready, kSoft * 32);
@@ -463,14 +461,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRestRegs));
     if (warp == W_MMA_P) {
     // ================================================================ MMA issuer
-    // Tiles in the order of use: K of the first kSBufs, then per tile i the K of
-    // tile i + kSBufs (if any) and the V of tile i.
+    // Tiles in the order of use: K of the first, then per tile i the K of tile
+    // i + 1 (if any) and the V of tile i.
     Walk walk(P);
     Segment G = {};
     uint32_t buf = 0, tile = 0, item = 0;
     bool ok = true;
-    auto qk = [&](uint32_t t) -> bool {             // S of tile t (counted over the CTA)
-      const uint32_t sb = t % L::kSBufs;
+    auto qk = [&]() -> bool {                       // S of the next tile
 #pragma unroll
       for (int u = 0; u < L::kUnits; ++u, ++buf) {
         const uint32_t x = buf % kBufs;
@@ -481,10 +478,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           constexpr int kSteps = D / 16 / L::kUnits;
 #pragma unroll
           for (int k = 0; k < kSteps; ++k)
-            mma_ts(tmem + L::kS + sb * T, tmem + L::kQ + 8 * (u * kSteps + k),
+            mma_ts(tmem + L::kS, tmem + L::kQ + 8 * (u * kSteps + k),
                    gemm::desc_sw128(at + (k >> 2) * (T * 128)) + 2 * (k & 3), idesc(T, false), u > 0 || k > 0);
           tc_commit(kv_empty + 8 * x);
-          if (u + 1 == L::kUnits) tc_commit(s_full + 8 * sb);
+          if (u + 1 == L::kUnits) tc_commit(s_full);
         }
         __syncwarp();
       }
@@ -494,15 +491,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       if (!mbar_wait_warp(q_ready, item & 1, abort_flag, A.dev_status)) { ok = false; break; }
       tc_fence_after();
       const int n = G.s1 - G.s0;
-      for (int i = 0; ok && i < L::kSBufs && i < n; ++i) ok = qk(tile + i);
+      ok = qk();
       for (int i = 0; ok && i < n; ++i, ++tile) {
-        if (i + L::kSBufs < n) {
-          const uint32_t sb = tile % L::kSBufs;
-          if (!mbar_wait_warp(s_free + 8 * sb, (tile / L::kSBufs) & 1, abort_flag, A.dev_status) ||
-              !qk(tile + L::kSBufs)) {
-            ok = false;
-            break;
-          }
+        if (i + 1 < n && (!mbar_wait_warp(s_free, tile & 1, abort_flag, A.dev_status) || !qk())) {
+          ok = false;
+          break;
         }
         if (!mbar_wait_warp(p_full, tile & 1, abort_flag, A.dev_status)) { ok = false; break; }
 #pragma unroll
@@ -519,12 +512,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
                 mma_ss(tmem + L::kO, gemm::desc_sw128(sbase + L::kPAt + u * (kRows * 128)) + 2 * k,
                        desc_n_major(at + k * 2048, kKeys * 128), idesc(D, true), i > 0 || u > 0 || k > 0);
               else
-                mma_ts(tmem + L::kO, tmem + L::kP + 8 * k, desc_n_major(at + k * 2048, kKeys * 128), idesc(D, true),
+                mma_ts(tmem + L::kO, tmem + L::kP + (tile & 1) * (T / 2) + 8 * k, desc_n_major(at + k * 2048, kKeys * 128), idesc(D, true),
                        i > 0 || k > 0);
             }
             tc_commit(kv_empty + 8 * x);
             if (u + 1 == L::kUnits) {
-              tc_commit(pv_done + 8 * (tile & 1));
+              tc_commit(pv_done);
               if (i + 1 == n) tc_commit(o_done);
             }
           }
@@ -579,14 +572,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     };
     while (ok && walk.next(P, G)) {
       const int n = G.s1 - G.s0;
-      // K kSBufs tiles ahead of V; a tile's pages are read a step or more ahead
-      // of its K and kept until V's turn
-      constexpr int a = L::kSBufs;
-      int32_t p0 = fetch(0), p1 = fetch(1), p2 = a == 2 ? fetch(2) : -1;
-      for (int i = -a; ok && i < n; ++i) {
-        const int32_t p3 = i >= 0 ? fetch(i + a + 1) : -1;
-        const int k = i + a;
-        const int32_t pk = k == 0 ? p0 : a == 1 || k == 1 ? p1 : p2;
+      // K a tile ahead of V; a tile's pages are read a step ahead of its K and
+      // kept until V's turn
+      int32_t p0 = fetch(0), p1 = fetch(1);
+      for (int i = -1; ok && i < n; ++i) {
+        const int32_t p2 = i >= 0 ? fetch(i + 2) : -1;
+        const int k = i + 1;
+        const int32_t pk = i < 0 ? p0 : p1;
         if (k < n) {
           if (__any_sync(0xffffffffu, pk == -2)) {
             if (pk == -2) report(A.dev_status, NVFP4_ERR_INDEX);
@@ -597,8 +589,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
         if (i >= 0) {
           if (ok) ok = copy(p0, i, A.v_q, A.v_sf);
           p0 = p1;
-          if (a == 2) { p1 = p2; p2 = p3; }
-          else p1 = p3;
+          p1 = p2;
         }
       }
       tile += n;
@@ -639,9 +630,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     while (ok && walk.next(P, G)) {
       const int n = G.s1 - G.s0;
       for (int j = 0; ok && j < 2 * n; ++j, ++load) {
-        // kSBufs tiles of K first, then K and V in turn, then the last V
-        const int first = min(L::kSBufs + 0, n);
-        const bool is_v = j >= first && (j >= 2 * n - first || ((j - first) & 1) != 0);
+        const bool is_v = j > 0 && ((j & 1) == 0 || j == 2 * n - 1);   // K, then K and V in turn, then V
         const uint32_t slot = load % L::kSlots;
         if (!mbar_wait_warp(staged + 8 * slot, (load / L::kSlots) & 1, abort_flag, A.dev_status)) { ok = false; break; }
 #pragma unroll
@@ -699,9 +688,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       if (r < g.nrows) {
         const uint16_t *q = A.q + (int64_t)(g.seq.first + qi) * A.ld_q + (int64_t)h * D + side * (D / 2);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + 8 * i));
-          qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
+        for (int i = 0; i < D / 32; ++i) {
+          uint4 v, w;
+          load_block(q + 16 * i, A.v8_q, v, w);           // a whole sector a lane
+          qw[8 * i] = v.x; qw[8 * i + 1] = v.y; qw[8 * i + 2] = v.z; qw[8 * i + 3] = v.w;
+          qw[8 * i + 4] = w.x; qw[8 * i + 5] = w.y; qw[8 * i + 6] = w.z; qw[8 * i + 7] = w.w;
         }
       } else {
 #pragma unroll
@@ -742,44 +733,39 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       float m = kFloor, l = 0.0f;
       const int n = G.s1 - G.s0;
       for (int i = 0; i < n; ++i, ++tile) {
-        const uint32_t sb = tile % L::kSBufs;
-        ok &= mbar_wait_warp(s_full + 8 * sb, (tile / L::kSBufs) & 1, abort_flag, A.dev_status);
+        ok &= mbar_wait_warp(s_full, tile & 1, abort_flag, A.dev_status);
         tc_fence_after();
         uint32_t s[2][32];                                // this thread's 64 scores
-        tm_ld_begin(tmem + lanes + L::kS + sb * T + side * 64, s[0]);
-        tm_ld_begin(tmem + lanes + L::kS + sb * T + side * 64 + 32, s[1]);
+        tm_ld_begin(tmem + lanes + L::kS + side * 64, s[0]);
+        tm_ld_begin(tmem + lanes + L::kS + side * 64 + 32, s[1]);
         tm_ld_end(s[0]);
         tm_ld_end(s[1]);
         tc_fence_before();
-        mbar_arrive(s_free + 8 * sb);
+        mbar_arrive(s_free);
         const int tok0 = (G.s0 + i) * T + side * 64;
         const bool bad = bad_tag[tile & 15] == (int)tile + 1;
         if (__any_sync(0xffffffffu, limit - tok0 < 64) || bad) mask_scores(A, G, s, limit - tok0, tok0, bad);
         uint32_t p[32];
         float sum = 0.0f;
         if (i > 0) sum = weights(s, sc, m, p);
-        // Does the row's sum, over both threads, call for a larger maximum?  (A
-        // buffer of xch per tile parity: the last reads of one are a barrier back.)
-        volatile float *x = xch + (tile & 1) * 2 * kRows;
-        x[side * kRows + r] = sum;
-        pair_sync(quad);
-        const bool over = i == 0 || sum + x[(side ^ 1) * kRows + r] > kMostSum;
-        if (__any_sync(0xffffffffu, over)) {              // the same in both warps of the rows
+        // Do the weights of any of the 32 rows call for larger maxima?
+        if (pair_any(quad, i == 0 || sum > kMostSum)) {
           float top = __uint_as_float(s[0][0]);
 #pragma unroll
           for (int k = 1; k < 63; k += 2)
             top = max3(top, __uint_as_float(s[k >> 5][k & 31]), __uint_as_float(s[(k + 1) >> 5][(k + 1) & 31]));
           top = fmaxf(top, __uint_as_float(s[1][31]));
-          pair_sync(quad);                                // both have read the sums
+          // (a buffer of xch per tile parity: its last readers have met since)
+          volatile float *x = xch + (tile & 1) * 2 * kRows;
           x[side * kRows + r] = top;
           pair_sync(quad);
           top = fmaxf(top, x[(side ^ 1) * kRows + r]);
-          const float to = over ? fmaxf(m, top == -INFINITY ? -INFINITY : top * sc) : m;
+          const float to = fmaxf(m, top == -INFINITY ? -INFINITY : top * sc);
           const float f = ex2(m - to);
           m = to;
           l *= f;
           if (i > 0) {                                    // O by the new maximum, half of the row each
-            ok &= mbar_wait_warp(pv_done + 8 * ((tile - 1) & 1), ((tile - 1) >> 1) & 1, abort_flag, A.dev_status);
+            ok &= mbar_wait_warp(pv_done, (tile - 1) & 1, abort_flag, A.dev_status);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -794,20 +780,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           sum = weights(s, sc, m, p);
         }
         l += sum;
-        // ---- P for the MMA, once P V of the tile before is over.  (Two barriers
-        // in turn: of the one waited for, every earlier phase is over, since S of
-        // this tile was committed behind the P V of three tiles back.)
-        if (tile > 0)
-          ok &= mbar_wait_warp(pv_done + 8 * ((tile - 1) & 1), ((tile - 1) >> 1) & 1, abort_flag, A.dev_status);
+        // ---- P for the MMA.  The one tile in shared memory is free once P V of the
+        // tile before is over.  Of the two in tensor memory this one is free: S of
+        // this tile was committed behind the P V that used it last.
         if (L::kPShared) {
+          if (tile > 0) ok &= mbar_wait_warp(pv_done, (tile - 1) & 1, abort_flag, A.dev_status);
           uint8_t *at = smem + L::kPAt + side * (kRows * 128) + r * 128;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<uint4 *>(at + ((k ^ (r & 7)) << 4)) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {
-          tc_fence_after();
-          tm_st32(tmem + lanes + L::kP + side * 32, p);
+          tm_st32(tmem + lanes + L::kP + (tile & 1) * (T / 2) + side * 32, p);
           tm_wait_st();
         }
         tc_fence_before();
@@ -836,17 +820,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
         tm_ld32(tmem + lanes + L::kO + 32 * c, o);
         if (live && ok) {
           if (whole && A.out_bf16) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(A.out) + at * D + 32 * c);
+            uint16_t *dst = static_cast<uint16_t *>(A.out) + at * D + 32 * c;
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+            for (int j = 0; j < 16; ++j)
+              w[j] = bf16x2_of(pair_f32(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f));
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                    : "=r"(w[j])
-                    : "f"(__uint_as_float(o[8 * k + 2 * j + 1]) * f), "f"(__uint_as_float(o[8 * k + 2 * j]) * f));
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 2; ++j)
+              store_block(dst + 16 * j, A.v8_out, make_uint4(w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3]),
+                          make_uint4(w[8 * j + 4], w[8 * j + 5], w[8 * j + 6], w[8 * j + 7]));
           } else {
             float4 *dst = reinterpret_cast<float4 *>(
                 whole ? static_cast<float *>(A.out) + at * D + 32 * c : P.ws_o + (slot * kRows + r) * D + 32 * c);
