@@ -69,7 +69,7 @@ static_assert(32 * (kSoft * kSoftRegs + kConv * kConvRegs + 4 * kRestRegs) <= kP
 // What an item costs besides its tiles (Q in, the first S, O out), in tiles:
 // the line that is cut over the CTAs counts it, so that a CTA with many short
 // items takes no longer than the others.
-constexpr int kItemCost = 5;
+constexpr int kItemCost = 3;
 // A tile's weights may add up to this before the maximum is raised: every
 // weight then is an f16 (65504 is the largest).
 constexpr float kMostSum = 8192.0f;
