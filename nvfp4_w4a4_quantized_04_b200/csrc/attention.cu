@@ -26,6 +26,11 @@
 //    turns into the second one's B operand by an 8x8 transpose (movmatrix).
 //  * Every warp has its own ring of cp.async stages (32 tokens of K and V) and
 //    its own softmax state; warps meet only at the end of an item.
+//  * 32 rows of 256 elements leave no registers for the output in one warp.
+//    There a team of two warps shares a step: each takes the scores of one half
+//    of its tokens for all rows and the outputs of one half of the head, so
+//    every element is still converted once.  They show each other P in shared
+//    memory, with one barrier a step, which is also the vote below.
 //  * The weights are taken by the running maximum as it stands, which is raised
 //    only when a lane's weights of a step add up to more than 2^13 (P stays
 //    below f16's range): the usual step has one vote instead of a maximum, a
@@ -33,10 +38,18 @@
 // Q is brought to f16 by a power of two per row that puts the row's largest
 // element at 2^14: exact for every element within 2^29 of it.
 //
-// Split.  All items' steps (32 tokens each) form one line that is cut evenly
-// over the CTAs, so ragged batches, one long sequence and many short ones all
-// fill the GPU; an item that several CTAs share is joined by a second kernel
-// from (max, sum, unnormalized O) parts in the workspace.
+// Split.  All items' steps (32 tokens each, and kItemSteps for an item's begin
+// and end) form one line that is cut evenly over the CTAs, so ragged batches,
+// one long sequence and many short ones all fill the GPU; an item that several
+// CTAs share is joined by a second kernel from (max, sum, unnormalized O) parts
+// in the workspace.
+//
+// Measured, with the join: 64 sequences of up to 16 Ki tokens, 8 KV heads of 128
+// and 4 heads each: 135 us, 4.7 TB/s (72 % of a copy's rate); one of 256 Ki
+// tokens, 4 KV heads of 256 and 8 heads each: 68 us, 4.4 TB/s; 32 of 8 Ki with 4
+// queries of 8 heads on 4 of 256: 86 us.  What bounds it is the issue of the
+// conversions (about 600 warp instructions a step at D 128); more warps a SM
+// with fewer registers each are slower.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -49,6 +62,11 @@ namespace nvfp4 {
 namespace attn {
 
 constexpr int kStep = 32;                // tokens per step
+// What an item's begin and end (page ids, Q, the first loads' latency, the join
+// of the warps) weigh in the even split, in steps.  64 sequences of 982..16384
+// tokens with 8 KV heads of 128: 148 us at 0, 140 at 8, 135 at 16, 137 at 32,
+// 143 at 64; 32 of 4 queries with 4 KV heads of 256: 104, 94, 86, 91, 104 us.
+constexpr int kItemSteps = 16;
 // A step's weights of one lane may add up to this before the maximum is raised:
 // every weight then is an f16 (65504 is the largest).
 constexpr float kMostSum = 8192.0f;
@@ -107,32 +125,48 @@ __device__ __forceinline__ int v_piece(int t, int c) {
   return (pos ^ sw) * 16;
 }
 
-template <int D, int NT, int kStages, int kWarps>
+// kTeam warps share a step; a CTA has kWarps / kTeam teams.
+template <int D, int NT, int kStages, int kWarps, int kTeam>
 struct Layout {
-  static constexpr int R = 8 * NT;
+  static constexpr int R = 8 * NT, kTeams = kWarps / kTeam;
   static constexpr int kStageBytes = 2 * Half<D>::kBytes;
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kRing = kTeams * kStages * kStageBytes;
   static constexpr int kRS = D + 20;                      // row stride of the O exchange, in floats
-  static constexpr int kO = kWarps * R * kRS * 4;
+  static constexpr int kO = kTeams * R * kRS * 4;
   static constexpr int kMain = kRing > kO ? kRing : kO;
   static constexpr int kQ = kMain;                        // Q fragments: NT * (D/16) * 32 lanes * 8 bytes
   static constexpr int kRow = kQ + NT * (D / 16) * 256;   // per row: scale, limit
   static constexpr int kMl = kRow + R * 8;                // per warp and row: max, sum
-  static constexpr int kScan = kMl + kWarps * R * 8;      // scan scratch
+  static constexpr int kTop = kMl + kWarps * R * 8;       // per warp of a team and row: max of a step
+  static constexpr int kP = kTop + (kTeam == 2 ? kWarps * R * 4 : 0);       // per warp: its P of two steps
+  static constexpr int kScan = kP + (kTeam == 2 ? kWarps * 2 * NT * 256 : 0);   // scan scratch
   static constexpr int kPrefix = kScan + 64;
   static constexpr int bytes(int batch) { return kPrefix + 4 * (batch + 2); }
 };
 
-template <int D, int NT, int kStages, int kWarps, int kMinCtas>
+// Barrier of the two warps of team `team`, true when `any` holds in one of them.
+__device__ __forceinline__ bool team_any(int team, bool any) {
+  uint32_t r;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q;}"
+      : "=r"(r) : "r"((uint32_t)any), "r"(team + 1) : "memory");
+  return r != 0;
+}
+
+template <int D, int NT, int kStages, int kWarps, int kMinCtas, int kTeam>
 __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const DecodeArgs P) {
-  using L = Layout<D, NT, kStages, kWarps>;
-  constexpr int kThreads = kWarps * 32;
+  using L = Layout<D, NT, kStages, kWarps, kTeam>;
+  static_assert(kTeam == 1 || (kTeam == 2 && D == 256), "the halves of V are cut for D = 256");
+  constexpr int kThreads = kWarps * 32, kTeams = L::kTeams;
+  constexpr int kH = 2 / kTeam;          // halves of a step whose scores a warp takes
   using H = Half<D>;
   constexpr int R = L::R;
-  constexpr int J = D / 16;              // k-steps of S, m-tiles of O
+  constexpr int J = D / 16;              // k-steps of S
+  constexpr int JO = J / kTeam;          // m-tiles of O: the team's warps share the head dimension
   extern __shared__ __align__(128) uint8_t smem[];
   const Args &A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int team = warp / kTeam, half = warp % kTeam;
   float2 *s_row = reinterpret_cast<float2 *>(smem + L::kRow);
   float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kMl);
   int32_t *s_scan = reinterpret_cast<int32_t *>(smem + L::kScan);
@@ -155,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     for (int b = b0; b < b1; ++b) {
       int steps;
       seq_steps(P, load_seq(A, b), steps);
-      const int n = steps * A.heads_kv;
+      const int n = steps ? (steps + kItemSteps) * A.heads_kv : 0;
       s_prefix[b] = n;
       local += n;
     }
@@ -178,7 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     __syncthreads();
   }
   const int total = s_prefix[A.batch];
-  const int per_cta = (int)kv::steps_per_cta(total, gridDim.x, kWarps)     /* one step per warp at least */;
+  const int per_cta = (int)kv::steps_per_cta(total, gridDim.x, kTeams);    // one step per team at least
   if (blockIdx.x == 0) {
     for (int b = tid; b <= A.batch; b += kThreads) P.ws_head[b] = s_prefix[b];
     if (tid == 0) P.ws_head[A.batch + 1] = per_cta;
@@ -197,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
   const float kgs = __ldg(A.k_gs), vgs = __ldg(A.v_gs);
   int pos = (int)min((int64_t)total, (int64_t)blockIdx.x * per_cta);
   const int end = (int)min((int64_t)total, (int64_t)pos + per_cta);
-  const uint32_t ring = smem_addr(smem) + warp * kStages * L::kStageBytes;
+  const uint32_t ring = smem_addr(smem) + team * kStages * L::kStageBytes;
   const uint32_t qs = smem_addr(smem + L::kQ) + lane * 8;
 
   while (pos < end) {
@@ -206,8 +240,11 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     int steps;
     seq_steps(P, seq, steps);
     const int local = pos - s_prefix[b];
-    const int head = local / steps, s0 = local - head * steps;
-    const int s1 = min(steps, s0 + (end - pos));
+    const int head = local / (steps + kItemSteps), start = s_prefix[b] + head * (steps + kItemSteps);
+    pos = min(end, start + kItemSteps + steps);
+    int s0, s1;
+    kv::item_part(blockIdx.x, per_cta, start, kItemSteps, steps, s0, s1);
+    if (s0 == s1) continue;              // only the item's fixed part lies in this range
     const int nrows = seq.queries * A.group;
 
     // ---- Q fragments: one warp per row, f16 with a power of two per row
@@ -275,9 +312,9 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     // what every row sees (the rows that pad the block see nothing: they count as the first row)
     const int lim_min = (int)kv::visible_keys(seq.len, seq.queries, 0, A.causal != 0);
 
-    float o[J][NT][4];
+    float o[JO][NT][4];
 #pragma unroll
-    for (int i = 0; i < J; ++i)
+    for (int i = 0; i < JO; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -292,11 +329,11 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
         l[nt][i] = 0.0f;
       }
 
-    // ---- the warp's steps: s0 + warp, + kWarps, ...
-    const int mine = max(0, (s1 - s0 - warp + kWarps - 1) / kWarps);
+    // ---- the team's steps: s0 + team, + kTeams, ...
+    const int mine = max(0, (s1 - s0 - team + kTeams - 1) / kTeams);
     int64_t base_reg = -1;               // lane i: pool row of half (i & 1) of iteration (block of 16) + i / 2
     auto fetch_pages = [&](int it0) {
-      const int tok = (s0 + warp + (it0 + (lane >> 1)) * kWarps) * kStep + (lane & 1) * 16;
+      const int tok = (s0 + team + (it0 + (lane >> 1)) * kTeams) * kStep + (lane & 1) * 16;
       base_reg = -1;
       if (it0 + (lane >> 1) < mine && tok < seq.len) {
         const int e = (int)fast_div((uint32_t)tok, A.by_page);
@@ -313,7 +350,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
         if ((it & 15) == 0) fetch_pages(it);
         const int stage = it % kStages;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int hh = 0; hh < kH; ++hh) {
+          const int h = hh + half;
           const int64_t base = __shfl_sync(0xffffffffu, base_reg, 2 * (it & 15) + h);
           const uint32_t dst = ring + stage * L::kStageBytes + h * H::kBytes;
           valid &= ~(1u << (2 * stage + h));
@@ -340,19 +378,20 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     for (int i = 0; i < kStages - 1; ++i) load_stage(i);
 
     for (int it = 0; it < mine; ++it) {
-      load_stage(it + kStages - 1);
-      cp_async_wait<kStages - 1>();
+      // a team's stages are free for the next load only behind its barrier below
+      if constexpr (kTeam == 1) load_stage(it + kStages - 1);
+      cp_async_wait<kStages - kTeam>();
       __syncwarp();
       const int stage = it % kStages;
       const uint32_t st = ring + stage * L::kStageBytes;
-      const int tok0 = (s0 + warp + it * kWarps) * kStep;
+      const int tok0 = (s0 + team + it * kTeams) * kStep;
 
       // S^T: tokens g and g + 8 of each half against the rows 2 t4, 2 t4 + 1.
-      // Both halves side by side: each fragment of Q is read once, and their
+      // A lone warp's halves go side by side: each fragment of Q is read once, and their
       // chains of MMAs are independent.
-      float s[2][NT][4];
+      float s[kH][NT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kH; ++h)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -360,10 +399,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
       constexpr int kPieces = D == 256 ? 2 : 1, kWords = D == 64 ? 2 : 4;
 #pragma unroll
       for (int pc = 0; pc < kPieces; ++pc) {
-        uint32_t ka[2][4], kb[2][4], sa[2], sb[2];
+        uint32_t ka[kH][4], kb[kH][4], sa[kH], sb[kH];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t hb = st + h * H::kBytes;
+        for (int h = 0; h < kH; ++h) {
+          const uint32_t hb = st + (h + half) * H::kBytes;
           if constexpr (D == 64) {
             const uint2 x = lds_v2(hb + H::kK + g * 32 + t4 * 8), y = lds_v2(hb + H::kK + (g + 8) * 32 + t4 * 8);
             ka[h][0] = x.x; ka[h][1] = x.y; kb[h][0] = y.x; kb[h][1] = y.y;
@@ -388,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
             q1[nt] = lds_v2(qs + (nt * J + j + 1) * 256);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kH; ++h) {
             const uint32_t fa = e4m3_pair_f16x2(__byte_perm(sa[h], 0, w < 2 ? 0x2020 : 0x2121));
             const uint32_t fb = e4m3_pair_f16x2(__byte_perm(sb[h], 0, w < 2 ? 0x2020 : 0x2121));
             const uint32_t a = ka[h][w], b = kb[h][w];
@@ -408,27 +447,28 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
       // The weights by the maximum as it stands; only when a lane's weights of
       // this step add up to too much is the maximum raised and all of them taken
       // again.  Steps that every row sees whole need no mask.
-      const bool all = tok0 + kStep <= lim_min && ((valid >> (2 * stage)) & 3) == 3;
+      const uint32_t have = valid >> (2 * stage + half);
+      const bool all = tok0 + kStep <= lim_min && (have & (kH == 2 ? 3 : 1)) == (kH == 2 ? 3 : 1);
       if (!all) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool ok = (valid >> (2 * stage + h)) & 1;
+        for (int h = 0; h < kH; ++h) {
+          const bool ok = (have >> h) & 1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (!ok || tok0 + 16 * h + g + (k >> 1) * 8 >= lim[nt][k & 1]) s[h][nt][k] = -INFINITY;
+              if (!ok || tok0 + 16 * (h + half) + g + (k >> 1) * 8 >= lim[nt][k & 1]) s[h][nt][k] = -INFINITY;
         }
       }
-      uint32_t pb[2][NT][2];
+      uint32_t pb[2][NT][2];             // of the halves [kH] first
       float sum[NT][2];
       auto take = [&]() {
         float most = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[2][4];
+          float p[kH][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kH; ++h) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) p[h][k] = ex2(fmaf(s[h][nt][k], sc[nt][k & 1], -m[nt][k & 1]));
             pb[h][nt][0] = pack_f16x2(p[h][0], p[h][1]);
@@ -436,54 +476,118 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            sum[nt][i] = (p[0][i] + p[0][i + 2]) + (p[1][i] + p[1][i + 2]);
+            sum[nt][i] = p[0][i] + p[0][i + 2];
+            if constexpr (kH == 2) sum[nt][i] += p[1][i] + p[1][i + 2];
             most = fmaxf(most, sum[nt][i]);
           }
         }
-        return most;
+        return most > kMostSum;
       };
-      if (__any_sync(0xffffffffu, take() > kMostSum)) {
+      auto turn = [&]() {                // tokens as rows -> the second MMA's B operand
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            pb[h][nt][0] = transpose8x8(pb[h][nt][0]);
+            pb[h][nt][1] = transpose8x8(pb[h][nt][1]);
+          }
+      };
+      // A team's warps show each other their P: two buffers, since the partner may
+      // still read the one before.
+      const uint32_t p_mine = smem_addr(smem + L::kP) + ((warp * 2 + (it & 1)) * NT * 32 + lane) * 8;
+      auto show = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sts_v2(p_mine + nt * 256, pb[0][nt][0], pb[0][nt][1]);
+      };
+      bool raise = take();
+      if constexpr (kTeam == 1) {
+        raise = __any_sync(0xffffffffu, raise);
+      } else {
+        turn();
+        show();
+        raise = team_any(team, raise);
+        load_stage(it + kStages - 1);
+      }
+      if (raise) {
+        float x[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x == -INFINITY ? x : x * sc[nt][i], m[nt][i]);
-            const float f = ex2(m[nt][i] - x);
-            m[nt][i] = x;
+            float y = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+            if constexpr (kH == 2) y = fmaxf(y, fmaxf(s[1][nt][i], s[1][nt][i + 2]));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            x[nt][i] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          }
+        if constexpr (kTeam == 2) {
+          float *top = reinterpret_cast<float *>(smem + L::kTop) + team * 2 * R;
+          if (g == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              *reinterpret_cast<float2 *>(top + half * R + 8 * nt + 2 * t4) = make_float2(x[nt][0], x[nt][1]);
+          team_any(team, false);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 y = *reinterpret_cast<const float2 *>(top + (half ^ 1) * R + 8 * nt + 2 * t4);
+            x[nt][0] = fmaxf(x[nt][0], y.x);
+            x[nt][1] = fmaxf(x[nt][1], y.y);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y = x[nt][i];
+            const float to = fmaxf(y == -INFINITY ? y : y * sc[nt][i], m[nt][i]);
+            const float f = ex2(m[nt][i] - to);
+            m[nt][i] = to;
             l[nt][i] *= f;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
+            for (int j = 0; j < JO; ++j) {
               o[j][nt][i] *= f;
               o[j][nt][i + 2] *= f;
             }
           }
         take();
+        if constexpr (kTeam == 2) {
+          turn();
+          show();
+          team_any(team, false);
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         l[nt][0] += sum[nt][0];
         l[nt][1] += sum[nt][1];
+      }
+      if constexpr (kTeam == 1) {
+        turn();
+      } else {
+        const uint32_t p_other = p_mine + (half ? -1 : 1) * (2 * NT * 256);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          pb[h][nt][0] = transpose8x8(pb[h][nt][0]);
-          pb[h][nt][1] = transpose8x8(pb[h][nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 x = lds_v2(p_other + nt * 256);
+          pb[1][nt][0] = x.x;
+          pb[1][nt][1] = x.y;
         }
       }
 
-      // O^T += V^T P^T: lane (g, t4) holds head elements [g D/8, (g+1) D/8) of tokens 2 t4, 2 t4 + 1, + 8, + 9
+      // O^T += V^T P^T: lane (g, t4) holds head elements [g D/8, (g+1) D/8) of tokens 2 t4, 2 t4 + 1, + 8, + 9;
+      // a team's warps take one half of each such run
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t hb = st + h * H::kBytes;
-        constexpr int kWords = D / 64;
+        const uint32_t hb = st + (kTeam == 1 ? h : h ^ half) * H::kBytes;
+        constexpr int kWords = D / 64 / kTeam;
         uint32_t v[4][kWords], vs[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int t = 2 * t4 + (k & 1) + (k >> 1) * 8;
-          if constexpr (D == 256) {
+          if constexpr (kTeam == 2) {
+            const uint2 x = lds_v2(hb + H::kV + v_piece<D>(t, g) + half * 8);
+            v[k][0] = x.x; v[k][1] = x.y;
+            vs[k] = lds_u8(hb + H::kVs + t * 16 + 2 * g + half);
+          } else if constexpr (D == 256) {
             const uint4 x = lds_v4(hb + H::kV + v_piece<D>(t, g));
             v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
             vs[k] = lds_u16(hb + H::kVs + t * 16 + 2 * g);
@@ -521,7 +625,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     }
     cp_async_wait<0>();
 
-    // ---- the four warps' states joined through shared memory
+    // ---- the warps' states joined through shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -535,26 +639,30 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
     __syncthreads();                     // every warp is done with its ring
     float *s_o = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < JO; ++j)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float *p = s_o + (warp * R + 8 * nt + 2 * t4) * L::kRS + g * (D / 8 + 2) + 2 * j;
+        float *p = s_o + (team * R + 8 * nt + 2 * t4) * L::kRS + g * (D / 8 + 2) + 2 * (j + half * JO);
         *reinterpret_cast<float2 *>(p) = make_float2(o[j][nt][0], o[j][nt][2]);
         *reinterpret_cast<float2 *>(p + L::kRS) = make_float2(o[j][nt][1], o[j][nt][3]);
       }
     __syncthreads();
     const bool whole = s0 == 0 && s1 == steps;
-    const int slot = 2 * blockIdx.x + kv::part_slot(blockIdx.x, per_cta, pos - s0);
+    const int slot = 2 * blockIdx.x + kv::part_slot(blockIdx.x, per_cta, start);
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      float2 ml[kWarps];
+      float2 ml[kTeams];
       float M = kFloor;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ml[w] = s_ml[w * R + r], M = fmaxf(M, ml[w].x);
+      for (int w = 0; w < kTeams; ++w) {
+        ml[w] = s_ml[w * kTeam * R + r];
+        if constexpr (kTeam == 2) ml[w].y += s_ml[(w * kTeam + 1) * R + r].y;
+        M = fmaxf(M, ml[w].x);
+      }
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kTeams; ++w) {
         const float f = ex2(ml[w].x - M);
         sum += f * ml[w].y;
         const float *p = s_o + (w * R + r) * L::kRS + d + 2 * (d / (D / 8));
@@ -572,24 +680,29 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
         if (d == 0) *reinterpret_cast<float2 *>(P.ws_ml + ((int64_t)slot * R + r) * 2) = make_float2(M, sum);
       }
     }
-    pos += s1 - s0;
   }
 }
 
-// Joins the items that several CTAs shared: CTA (c, r) row r of the item in
+// Joins the items that several CTAs shared: CTA (c, y) rows of the item in
 // which CTA c's range of the first kernel begins, if it began earlier and c is
-// the first to continue it.  kGroups groups of D/4 threads take every kGroups-th
-// part.
-constexpr int kJoin = 512;
-template <int D, int R>
-__global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
-  constexpr int kLanes = D / 4, kGroups = kJoin / kLanes;
-  __shared__ float4 s_o[kJoin];
-  __shared__ float s_sum[kGroups], s_max[kJoin / 32];
+// the first to continue it.  D/4 threads take a row.  kWide, for calls of few
+// items, each of many parts: a CTA has one row, whose parts its groups of
+// threads share.  Otherwise a group takes a row with all its parts.
+template <int D, int R, bool kWide>
+struct Join {
+  static constexpr int kLanes = D / 4;
+  static constexpr int kThreads = kWide || R * kLanes > 512 ? 512 : R * kLanes;
+  static constexpr int kGroups = kThreads / kLanes;
+  static constexpr int kRows = kWide ? 1 : kGroups;      // rows of a CTA
+};
+template <int D, int R, bool kWide>
+__global__ void __launch_bounds__(Join<D, R, kWide>::kThreads) combine_kernel(const DecodeArgs P) {
+  using J = Join<D, R, kWide>;
+  constexpr int kLanes = J::kLanes, kThreads = J::kThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Args &A = P.a;
   const int tid = threadIdx.x, lane = tid % kLanes, part = tid / kLanes;
-  const int r = blockIdx.y, c = blockIdx.x + 1;
+  const int r = kWide ? blockIdx.y : blockIdx.y * J::kRows + part, c = blockIdx.x + 1;
   const int per = P.ws_head[A.batch + 1], total = P.ws_head[A.batch];
   const int64_t pos = (int64_t)c * per;
   if (per == 0 || pos >= total) return;  // refused offsets; or a CTA without work
@@ -597,40 +710,49 @@ __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
   const Seq seq = load_seq(A, b);
   int steps;
   if (!seq_steps(P, seq, steps) || r >= seq.queries * A.group) return;
-  const int head = ((int)pos - P.ws_head[b]) / steps;
-  const int start = P.ws_head[b] + head * steps;
+  const int head = ((int)pos - P.ws_head[b]) / (steps + kItemSteps);
+  const int start = P.ws_head[b] + head * (steps + kItemSteps);
   if (start == pos || (int64_t)(c - 1) * per > start) return;
-  const int c0 = c - 1, c1 = (start + steps - 1) / per;
+  const int c0 = (start + kItemSteps) / per, c1 = (start + kItemSteps + steps - 1) / per;
+  if (c0 == c1) return;                  // one CTA had all of its steps
+  auto slot = [&](int k) { return (int64_t)(2 * k + kv::part_slot(k, per, start)) * R + r; };
   float M = kFloor, sum = 0.0f;
-  for (int k = c0 + tid; k <= c1; k += kJoin)
-    M = fmaxf(M, P.ws_ml[((int64_t)(2 * k + kv::part_slot(k, per, start)) * R + r) * 2]);
+  if constexpr (kWide) {
+    __shared__ float s_max[kThreads / 32];
+    for (int k = c0 + tid; k <= c1; k += kThreads) M = fmaxf(M, P.ws_ml[slot(k) * 2]);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if ((tid & 31) == 0) s_max[tid >> 5] = M;
-  __syncthreads();
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if ((tid & 31) == 0) s_max[tid >> 5] = M;
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kJoin / 32; ++k) M = fmaxf(M, s_max[k]);
+    for (int k = 0; k < kThreads / 32; ++k) M = fmaxf(M, s_max[k]);
+  } else {
+    for (int k = c0; k <= c1; ++k) M = fmaxf(M, P.ws_ml[slot(k) * 2]);
+  }
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int k = c0 + part; k <= c1; k += kGroups) {
-    const int64_t slot = (int64_t)(2 * k + kv::part_slot(k, per, start)) * R + r;
-    const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + slot * 2);
-    const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + slot * D + lane * 4);
+  for (int k = kWide ? c0 + part : c0; k <= c1; k += kWide ? J::kGroups : 1) {
+    const float2 ml = *reinterpret_cast<const float2 *>(P.ws_ml + slot(k) * 2);
+    const float4 x = *reinterpret_cast<const float4 *>(P.ws_o + slot(k) * D + lane * 4);
     const float f = ex2(ml.x - M);
     sum += f * ml.y;
     acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
   }
-  s_o[tid] = acc;
-  if (lane == 0) s_sum[part] = sum;
-  __syncthreads();
-  if (part) return;
-  sum = 0.0f;
-  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if constexpr (kWide) {
+    __shared__ float4 s_o[kThreads];
+    __shared__ float s_sum[J::kGroups];
+    s_o[tid] = acc;
+    if (lane == 0) s_sum[part] = sum;
+    __syncthreads();
+    if (part) return;
+    sum = 0.0f;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const float4 x = s_o[k * kLanes + lane];
-    sum += s_sum[k];
-    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    for (int k = 0; k < J::kGroups; ++k) {
+      const float4 x = s_o[k * kLanes + lane];
+      sum += s_sum[k];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
   }
   const int qi = r / A.group, h = head * A.group + r - qi * A.group;
   const int64_t at = (int64_t)(seq.first + qi) * A.heads_q + h;
@@ -639,34 +761,40 @@ __global__ void __launch_bounds__(kJoin) combine_kernel(const DecodeArgs P) {
   if (A.lse && lane == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
+template <int D, int R, bool kWide>
+bool launch_combine(const DecodeArgs &p, cudaStream_t stream) {
+  using J = Join<D, R, kWide>;
+  return launch_behind(combine_kernel<D, R, kWide>, dim3((unsigned)(p.grid - 1), (unsigned)(R / J::kRows)), J::kThreads, 0,
+                       stream, p);
+}
+
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Most rows of a sequence that the decode form takes (one row block: the
-// accumulators leave room for no more, and a second block would read the cache
-// again); sequences with more go to the prefill form.
-int row_limit(int D) { return D == 256 ? 16 : 32; }
+// Most rows of a sequence that the decode form takes (the accumulators leave
+// room for no more); sequences with more go to the prefill form.
+constexpr int kRowLimit = 32;
 
 // 8-row tiles of a row block that holds `rows` rows.
-int tiles_for(int64_t rows, int D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
+int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 // CTAs that the workspace is sized for: at most 4 per SM.
 int64_t max_grid() { return (int64_t)host::sm_count() * 4; }
 
 int64_t decode_workspace(int batch, int64_t rows, int D) {
-  const int64_t R = 8 * tiles_for(rows, D);
+  const int64_t R = 8 * tiles_for(rows);
   return align256(4 * ((int64_t)batch + 2)) + align256(2 * max_grid() * R * 8) + align256(2 * max_grid() * R * D * 4);
 }
 
-template <int D, int NT, int kStages, int kWarps, int kMinCtas>
+template <int D, int NT, int kStages, int kWarps, int kMinCtas, int kTeam = 1>
 nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t stream) {
-  using L = Layout<D, NT, kStages, kWarps>;
+  using L = Layout<D, NT, kStages, kWarps, kTeam>;
   constexpr int kThreads = kWarps * 32;
-  auto kern = decode_kernel<D, NT, kStages, kWarps, kMinCtas>;
+  auto kern = decode_kernel<D, NT, kStages, kWarps, kMinCtas, kTeam>;
   const int smem = L::bytes(p.a.batch);
   if (!host::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), L::bytes(kMaxBatch))) return NVFP4_ERR_CUDA;
   int64_t grid = (int64_t)host::sm_count() * host::blocks_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
   if (grid > max_grid()) grid = max_grid();
-  const int64_t want = (total_bound + kWarps - 1) / kWarps;
+  const int64_t want = (total_bound + L::kTeams - 1) / L::kTeams;
   if (grid > want) grid = want < 1 ? 1 : want;
   p.grid = (int32_t)grid;
   p.ws_head = reinterpret_cast<int32_t *>(ws);
@@ -677,7 +805,10 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
   if (grid == 1) return NVFP4_OK;
-  return launch_behind(combine_kernel<D, L::R>, dim3((unsigned)(grid - 1), (unsigned)L::R), kJoin, 0, stream, p)
+  // Few items have many parts each.  The other way round (128 items of 2 to 3 parts
+  // in 32 rows each), a CTA of 512 threads to a row takes 24 us instead of 9.
+  const bool wide = (int64_t)p.a.batch * p.a.heads_kv * 8 <= grid;
+  return (wide ? launch_combine<D, L::R, true>(p, stream) : launch_combine<D, L::R, false>(p, stream))
              ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
@@ -693,7 +824,7 @@ size_t nvfp4_paged_attention_workspace_size(int batch, int64_t max_query, int q_
     return 0;
   const int64_t rows = max_query * (q_heads / kv_heads);
   return (size_t)(decode_workspace(batch, rows, head_dim) +
-                  (rows > row_limit(head_dim) ? prefill_workspace(batch, max_query, q_heads / kv_heads, head_dim) : 0));
+                  (rows > kRowLimit ? prefill_workspace(batch, max_query, q_heads / kv_heads, head_dim) : 0));
 }
 
 nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, const int32_t *query_offsets,
@@ -726,13 +857,13 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   if (num_pages > 0 && (!k_q || !k_sf || !v_q || !v_sf)) return NVFP4_ERR_INVALID_ARG;
   const int group = q_heads / kv_heads;
   const int64_t rows = max_query * group;
-  const int cap = row_limit(head_dim);
+  const int cap = kRowLimit;
   // steps of the whole call: row blocks are bounded by the queries that there
   // are; the longest line is the prefill form's with 64-key tiles
   const int64_t keys = (int64_t)max_pages * page_size;
   const int64_t steps_max = (keys + kStep - 1) / kStep;
   const int64_t blocks = tokens * group / 128 + batch;
-  if ((int64_t)batch * kv_heads * steps_max > 0x3FFFFFFF || blocks * kv_heads * (keys / 64 + 1) > 0x3FFFFFFF ||
+  if ((int64_t)batch * kv_heads * (steps_max + kItemSteps) > 0x3FFFFFFF || blocks * kv_heads * (keys / 64 + 1) > 0x3FFFFFFF ||
       (int64_t)batch * ((rows + 127) / 128) > 0x3FFFFFFF)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   DecodeArgs p = {};
@@ -772,8 +903,8 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
         launch_prefill(p.a, head_dim, one_form ? 0 : cap, ws + decode_workspace(batch, rows, head_dim), stream);
     if (st != NVFP4_OK || one_form) return st;
   }
-  const int nt = tiles_for(rows, head_dim);
-  const int64_t total_bound = (int64_t)batch * kv_heads * steps_max;
+  const int nt = tiles_for(rows);
+  const int64_t total_bound = (int64_t)batch * kv_heads * (steps_max + kItemSteps);
   if (head_dim == 64) {
     if (nt == 1) return run<64, 1, 3, 8, 2>(p, total_bound, ws, stream);
     if (nt == 2) return run<64, 2, 3, 4, 3>(p, total_bound, ws, stream);
@@ -785,7 +916,8 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
     return run<128, 4, 3, 4, 2>(p, total_bound, ws, stream);
   }
   if (nt == 1) return run<256, 1, 2, 8, 1>(p, total_bound, ws, stream);
-  return run<256, 2, 2, 8, 1>(p, total_bound, ws, stream);
+  if (nt == 2) return run<256, 2, 2, 8, 1>(p, total_bound, ws, stream);
+  return run<256, 4, 4, 8, 1, 2>(p, total_bound, ws, stream);
 }
 
 }  // extern "C"

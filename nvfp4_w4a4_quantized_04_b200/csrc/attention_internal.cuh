@@ -9,7 +9,6 @@ namespace nvfp4 {
 namespace attn {
 
 constexpr float kFloor = -1e30f;         // running maximum before the first key
-constexpr float kLazy = 8.0f;            // growth (log2) that P may show before a rescale
 constexpr int kMaxBatch = 4096;
 
 // The power of two that brings a row of Q to f16: 2^(14 - e) for a row whose

@@ -465,6 +465,35 @@ def test_attention_rising_and_peaked_scores(D):
         assert err.max().item() <= 0, err.max().item()
 
 
+# up to 32 rows a KV head, in batches of many short items and of one long among many
+FEW_ROWS = [
+    # D, hkv, group, page, lengths, queries
+    (256, 1, 17, 16, [1, 15, 16, 17, 31, 32, 33, 1000], None),
+    (256, 2, 6, 32, [5000, 4, 640, 0, 129, 77], [4, 4, 3, 2, 1, 4]),
+    (256, 1, 32, 64, [3000], None),
+    (256, 4, 8, 32, [9 * i % 131 for i in range(64)], [1 + i % 4 for i in range(64)]),
+    (256, 1, 8, 16, [40000] + [20] * 60, [4] * 61),
+    (256, 1, 4, 64, [30000] + [70] * 60, None),
+    (128, 1, 8, 64, [60000] + [30] * 60, [2] * 61),
+    (64, 2, 2, 16, [30000] + [7] * 40, None),
+]
+
+
+@pytest.mark.parametrize("D,hkv,group,ps,lens,queries", FEW_ROWS)
+@pytest.mark.parametrize("spread", [None, 100.0])
+def test_attention_few_rows(D, hkv, group, ps, lens, queries, spread):
+    c = Case(sum(lens) + group, D, hkv, group, ps, lens, queries, True, **({} if spread is None else {"spread": spread}))
+    want, lse, mag = c.reference()
+    ls = torch.full(lse.shape, 5.0, dtype=torch.float32, device="cuda")
+    st = status_word()
+    out = c.run(out_dtype=layer().OUT_F32, lse=ls, dev_status=st)
+    assert st.item() == 0
+    err = (out.double() - want).abs() - c.tolerance(want, mag, torch.float32)
+    assert not torch.isnan(out).any() and err.max().item() <= 0, err.max().item()
+    empty = torch.isinf(lse)
+    assert torch.equal(empty, torch.isinf(ls)) and (out[empty] == 0).all()
+
+
 def test_attention_large_and_small_queries():
     """bf16 queries far outside f16's range are scaled by row."""
     c = Case(4, 128, 2, 4, 64, [200, 70], None, True, spread=2.0 ** -60)
