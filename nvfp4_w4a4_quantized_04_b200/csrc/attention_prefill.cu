@@ -90,8 +90,8 @@ template <int D> struct Pre {
   static constexpr int kCodeBytes = T * D / 2, kScaleBytes = T * D / 16, kSlotBytes = kCodeBytes + kScaleBytes;
   static constexpr int kStageAt = kPAt + kPBytes;
   static constexpr int kBar = kStageAt + kSlots * kSlotBytes;
-  // kv_full[], kv_empty[], s_full, s_free, pv_done, p_full, o_done, q_ready, drain, staged[], unstaged[]
-  static constexpr int kNumBars = 2 * kBufs + 7 + 2 * kSlots;
+  // kv_full[], kv_empty[], s_full, s_free, pv_done, p_full[2], o_done, q_ready, drain, staged[], unstaged[]
+  static constexpr int kNumBars = 2 * kBufs + 8 + 2 * kSlots;
   static constexpr int kMisc = kBar + kNumBars * 8;      // tmem base, abort flag, bad-page tags[16]
   static constexpr int kXch = kMisc + 8 + 64;            // [4][128] floats between a row's two threads
   static constexpr int kBytes = kXch + 4 * kRows * 4 + 1024;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
   const Args &A = P.a;
   const uint32_t sbase = smem_addr(smem);
   const uint32_t kv_full = sbase + L::kBar, kv_empty = kv_full + 8 * kBufs, s_full = kv_empty + 8 * kBufs;
-  const uint32_t s_free = s_full + 8, pv_done = s_free + 8, p_full = pv_done + 8, o_done = p_full + 8;
+  const uint32_t s_free = s_full + 8, pv_done = s_free + 8, p_full = pv_done + 8, o_done = p_full + 16;
   const uint32_t q_ready = o_done + 8, drain = q_ready + 8, staged = drain + 8, unstaged = staged + 8 * L::kSlots;
   volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     mbar_init(s_free, kSoft * 32);
     mbar_init(pv_done, 1);
     mbar_init(p_full, kSoft * 32);
+    mbar_init(p_full + 8, kSoft * 32);
     mbar_init(o_done, 1);
     mbar_init(q_ready, kSoft * 32);
     mbar_init(drain, 1);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           ok = false;
           break;
         }
-        if (!mbar_wait_warp(p_full, tile & 1, abort_flag, A.dev_status)) { ok = false; break; }
+        if (!mbar_wait_warp(p_full + 8 * (tile & 1), (tile >> 1) & 1, abort_flag, A.dev_status)) { ok = false; break; }
 #pragma unroll
         for (int u = 0; ok && u < L::kUnits; ++u, ++buf) {
           const uint32_t x = buf % kBufs;
@@ -795,7 +796,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           tm_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(p_full);
+        // One barrier per tile parity: a warp may be here with the next tile while
+        // another still raises its maxima.  It cannot be two tiles ahead, since S of
+        // that tile waits for every warp's s_free of the next one.
+        mbar_arrive(p_full + 8 * (tile & 1));
       }
       // ---- the item's last P V, then O out, each thread half of its row; the
       // next item's Q is on its way meanwhile

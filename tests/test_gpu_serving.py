@@ -494,6 +494,23 @@ def test_attention_few_rows(D, hkv, group, ps, lens, queries, spread):
     assert torch.equal(empty, torch.isinf(ls)) and (out[empty] == 0).all()
 
 
+@pytest.mark.parametrize("D,hkv,group,ps,lens,queries", [
+    (128, 8, 4, 64, [2048], [2048]),
+    (64, 8, 4, 32, [2048], [2048]),
+    (128, 2, 8, 128, [1500, 900, 1800], [700, 900, 1]),
+    (256, 4, 4, 64, [1500], [1500]),
+])
+@pytest.mark.parametrize("spread", [1.0, 3.0, 10.0])
+def test_attention_prompts_whose_maxima_rise_here_and_there(D, hkv, group, ps, lens, queries, spread):
+    """Several items a CTA, and rows whose maxima rise at some later tile while
+    the others' do not."""
+    c = Case(D + int(spread), D, hkv, group, ps, lens, queries, True, spread=spread)
+    want, _, mag = c.reference()
+    out = c.run(out_dtype=layer().OUT_F32)
+    err = (out.double() - want).abs() - c.tolerance(want, mag, torch.float32)
+    assert not torch.isnan(out).any() and err.max().item() <= 0, err.max().item()
+
+
 def test_attention_large_and_small_queries():
     """bf16 queries far outside f16's range are scaled by row."""
     c = Case(4, 128, 2, 4, 64, [200, 70], None, True, spread=2.0 ** -60)
