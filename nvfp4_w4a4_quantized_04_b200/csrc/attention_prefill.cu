@@ -642,10 +642,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           const int code_u = u * (is_v ? 64 * (D / 2) : 64), scale_u = u * (is_v ? 64 * (D / 16) : 8);
           const uint4 code = lds_v4(from + code_u + (is_v ? at_codes[1] : at_codes[0]));
           const uint32_t scale = lds_u16(from + scale_u + (is_v ? at_scale[1] : at_scale[0]));
-          if (u + 1 == L::kUnits) {
-            __syncwarp();                                 // every lane has read the slot
-            if (lane == 0) mbar_arrive(unstaged + 8 * slot);
-          }
           if (buf >= kBufs && !mbar_wait_warp(kv_empty + 8 * x, ((buf / kBufs) - 1) & 1, abort_flag, A.dev_status)) {
             ok = false;
             break;
@@ -666,6 +662,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           mbar_arrive(kv_full + 8 * x);
+          // Only now is the slot given back: every lane's reads are behind the fence, so
+          // that the next bulk copy into it (async proxy) cannot pass them.
+          if (u + 1 == L::kUnits) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unstaged + 8 * slot);
+          }
         }
       }
     }

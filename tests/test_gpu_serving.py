@@ -511,6 +511,23 @@ def test_attention_prompts_whose_maxima_rise_here_and_there(D, hkv, group, ps, l
     assert not torch.isnan(out).any() and err.max().item() <= 0, err.max().item()
 
 
+@pytest.mark.parametrize("D,hkv,group,ps,lens", [
+    (128, 8, 4, 64, [4096]),
+    (64, 8, 4, 64, [4096]),
+    (256, 4, 4, 64, [3000]),
+    (128, 4, 4, 16, [1000, 2000, 500]),
+])
+def test_attention_prompts_repeat_to_the_bit(D, hkv, group, ps, lens):
+    """Every run gives the same bits, with the cache in L2 or not."""
+    c = Case(D, D, hkv, group, ps, lens, lens, True)
+    first = c.run(out_dtype=layer().OUT_F32)
+    evict = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(100):
+        if i % 2:
+            evict.fill_(i)
+        assert torch.equal(c.run(out_dtype=layer().OUT_F32), first), i
+
+
 def test_attention_large_and_small_queries():
     """bf16 queries far outside f16's range are scaled by row."""
     c = Case(4, 128, 2, 4, 64, [200, 70], None, True, spread=2.0 ** -60)
