@@ -484,7 +484,9 @@ def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch
     p = out if out is not None else empty_packed(rows, K, 1, None, layout, x.device)
     if p.K != K or p.layout != layout or p.q.shape[0] < alloc_rows(rows, 1, False, layout):
         raise ValueError("out: a packed tensor of this K and layout with enough rows is wanted")
-    _same_device(x, global_scale, y, p.q)
+    if p.sf.numel() < sf_bytes(alloc_rows(rows, 1, False, layout), K):
+        raise ValueError("out: too few bytes of scales")
+    _same_device(x, global_scale, y, p.q, p.sf, dev_status)
     p.gs, p.offsets, p.num_groups, p.rows = global_scale, None, 1, rows
     with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
@@ -507,7 +509,7 @@ def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: 
         raise ValueError("scale: fp32 [rows] is wanted")
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
         raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
-    _same_device(x, q, scale, y)
+    _same_device(x, q, scale, y, dev_status)
     with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
                                    NORM_E4M3, scale, q, None, SF_ROWMAJOR, dev_status)
@@ -593,7 +595,7 @@ class PagedKVCache:
                 ld_qo = _heads(q_out, tokens, D, "q_out")
                 if q_out.shape != q.shape:
                     raise ValueError("q_out: the shape of q is wanted")
-        _same_device(self.k_q, k, v, slots, q, q_out, positions, rope)
+        _same_device(self.k_q, k, v, slots, q, q_out, positions, rope, dev_status)
         with _on(self.k_q):
             nvfp4_kv_append(k, ld_k, v, ld_v, tokens, self.heads, D, slots, q, ld_q, hq, q_out, ld_qo, positions, rope,
                             rows, rot, int(interleaved), self.k_gs, self.v_gs, self.k_q, self.k_sf, self.v_q,
@@ -640,7 +642,7 @@ class PagedKVCache:
             ws = self.k_q.new_empty(max(need, 1))
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
-        _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws)
+        _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws, dev_status)
         scale = D ** -0.5 if softmax_scale is None else softmax_scale
         with _on(self.k_q):
             nvfp4_paged_attention(q, ld_q, tokens, query_offsets, max_query, seq_lens, batch, page_table,

@@ -715,3 +715,121 @@ def test_norm_append_attend_as_a_layer_uses_them():
     # dequantize() rounds each value to bf16 (2^-8 of it): in v directly, in k through the scores
     ds = torch.einsum("chd,nhd->hcn", q.abs(), kd[:, hk].abs()).max().item() * D ** -0.5 * 2.0 ** -8
     assert ((out - want).abs() <= mag * (2.0 ** -8 + 2.0 ** -10 + 2 * ds)).all()
+
+
+def test_status_words_and_scales_elsewhere_are_refused():
+    L = layer()
+    c = Case(3, 64, 1, 2, 16, [20])
+    host = torch.zeros(1, dtype=torch.int32)
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    gs = torch.ones(1, device="cuda")
+    short = L.empty_packed(4, 64)
+    short.sf = short.sf[:16]
+    for call in (lambda: c.run(dev_status=host), lambda: L.add_rmsnorm_e4m3(x, w, dev_status=host),
+                 lambda: L.add_rmsnorm_nvfp4(x, w, gs, dev_status=host), lambda: L.add_rmsnorm_nvfp4(x, w, gs, out=short),
+                 lambda: c.cache.append(c.q[:, :1], c.q[:, :1], torch.zeros(1, dtype=torch.int64, device="cuda"),
+                                        dev_status=host)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("D,group", [(64, 33), (128, 48), (256, 64), (128, 200)])
+def test_attention_one_query_of_many_heads(D, group):
+    """More heads on one KV head than the few-row form takes."""
+    c = Case(group, D, 1, group, 32, [700, 0, 33, 128])
+    want, lse, mag = c.reference()
+    ls = torch.full(lse.shape, 5.0, dtype=torch.float32, device="cuda")
+    out = c.run(out_dtype=layer().OUT_F32, lse=ls)
+    err = (out.double() - want).abs() - c.tolerance(want, mag, torch.float32)
+    assert not torch.isnan(out).any() and err.max().item() <= 0
+    assert torch.equal(torch.isinf(lse), torch.isinf(ls))
+
+
+@pytest.mark.parametrize("queries", [False, True])
+def test_attention_largest_batch(queries):
+    lens = [(7 * i) % 40 for i in range(4096)]
+    counts = [min(n, 1 + i % 20) for i, n in enumerate(lens)] if queries else None
+    c = Case(5, 64, 1, 2, 16, lens, counts)
+    want, _, mag = c.reference()
+    out = c.run(out_dtype=layer().OUT_F32)
+    err = (out.double() - want).abs() - c.tolerance(want, mag, torch.float32)
+    assert not torch.isnan(out).any() and err.max().item() <= 0
+
+
+def test_attention_of_an_empty_pool():
+    L = layer()
+    gs = torch.ones(1, device="cuda")
+    cache = L.PagedKVCache.empty(0, 16, 2, 128, gs, gs)
+    q = torch.ones(3, 4, 128, dtype=torch.bfloat16, device="cuda")
+    for width in (0, 2):
+        st = status_word()
+        out = cache.attend(q, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                           torch.zeros(3, width, dtype=torch.int32, device="cuda"), dev_status=st)
+        assert (out == 0).all() and st.item() == 0
+    many = torch.ones(70, 4, 128, dtype=torch.bfloat16, device="cuda")
+    out = cache.attend(many, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, 0, dtype=torch.int32, device="cuda"),
+                       query_offsets=torch.tensor([0, 70], dtype=torch.int32, device="cuda"), max_query=70)
+    assert (out == 0).all()
+
+
+def test_attention_of_two_streams_at_once():
+    """Both forms at the same time, each with memory of its own."""
+    cases = [Case(1, 128, 8, 4, 64, [1500], [1500]), Case(2, 256, 4, 8, 64, [9000, 70, 800], None),
+             Case(3, 64, 4, 4, 32, [1000], [1000])]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    for _ in range(10):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.run())
+    torch.cuda.synchronize()
+    for w, gs in zip(want, got):
+        for y in gs:
+            assert torch.equal(y, w)
+
+
+def test_norm_and_append_in_a_graph():
+    """Captured once, replayed on new rows, slots and positions."""
+    L = layer()
+    torch.manual_seed(1)
+    T, H, D, hkv = 5, 256, 64, 2
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    w = torch.randn(H, device="cuda").to(torch.bfloat16)
+    gs = torch.tensor([0.01], device="cuda")
+    cache = L.PagedKVCache.empty(8, 16, hkv, D, gs, gs)
+    other = L.PagedKVCache.empty(8, 16, hkv, D, gs, gs)
+    for c in (cache, other):
+        for t in (c.k_q, c.k_sf, c.v_q, c.v_sf):
+            t.zero_()
+    rope = L.rope_table(200, D)
+    k, v, q = (torch.randn(T, n, D, device="cuda").to(torch.bfloat16) for n in (hkv, hkv, 4))
+    slots = torch.arange(T, device="cuda")
+    pos = torch.arange(T, device="cuda")
+
+    def step(c):
+        return L.add_rmsnorm_nvfp4(x, w, gs)[0], L.add_rmsnorm_e4m3(x, w)[:2], \
+            c.append(k, v, slots, q=q, positions=pos, rope=rope)
+
+    step(other)
+    torch.cuda.synchronize()
+    for t in (other.k_q, other.k_sf, other.v_q, other.v_sf):
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        packed, (e, scale), qr = step(cache)
+    for i in range(3):
+        x.copy_(torch.randn(T, H, device="cuda"))
+        k.copy_(torch.randn(T, hkv, D, device="cuda"))
+        slots.copy_(torch.tensor([17 * i, -1, 40 + i, 60, 127 - i], device="cuda"))
+        pos.copy_(torch.tensor([i, 3, 150, 7, 199 - i], device="cuda"))
+        g.replay()
+        p2, (e2, s2), q2 = step(other)
+        torch.cuda.synchronize()
+        rows = slice(0, T)
+        assert torch.equal(packed.q[rows], p2.q[rows]) and torch.equal(e, e2) and torch.equal(scale, s2)
+        assert torch.equal(qr, q2)
+        for a in ("k_q", "k_sf", "v_q", "v_sf"):
+            assert torch.equal(getattr(cache, a), getattr(other, a))
