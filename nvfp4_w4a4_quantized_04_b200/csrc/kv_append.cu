@@ -17,6 +17,10 @@
 // over the heads, so the table is read once per token instead of once per
 // head; the host cuts the heads into chunks until the grid fills the GPU, so
 // that a decode step's few tokens still spread over all SMs.
+//
+// Measured: 16384 tokens of 32 + 2 x 4 heads of 256: 157 us, 4.5 TB/s (69 % of a
+// copy's rate; the dequantization of the pool that the timed call also makes is
+// in it); 64 tokens 12 us with it, the latency of slot, table, load and store.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
