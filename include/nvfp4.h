@@ -533,7 +533,8 @@ nvfp4_status nvfp4_add_rmsnorm_quantize(const void *x, int64_t ld_x, const void 
  *   slots         int64 [tokens]; a negative slot skips the token's K and V
  *                 (padding); a slot past the pool skips them and reports
  *                 NVFP4_ERR_INDEX.  The slots written must be distinct: two
- *                 tokens with one slot leave either's elements there.
+ *                 tokens with one slot leave codes and scales of either there
+ *                 (finite values, which ones is not defined).
  *   q, q_out      nullable bf16 [tokens, q_heads, head_dim], strides ld_q,
  *                 ld_qo: rotated copy; q_out may be q itself, in place.
  *   rope          fp32 [rope_rows, rot_dim]: per position rot_dim/2 cosines,
@@ -544,6 +545,8 @@ nvfp4_status nvfp4_add_rmsnorm_quantize(const void *x, int64_t ld_x, const void 
  *   interleaved   0: element i pairs with i + rot_dim/2; 1: 2i with 2i + 1.
  *                 (a, b) -> (a c - b s, b c + a s), correctly rounded to bf16.
  *   k_gs, v_gs    fp32 [1], > 0: the encode is nvfp4_quantize's GIVEN mode.
+ *   k_q .. v_sf   the pool (as for nvfp4_paged_attention), each 16-byte aligned;
+ *                 may be NULL with num_pages == 0.
  *   dev_status    also NVFP4_ERR_NONFINITE: a 16-element block with a NaN or
  *                 inf is stored as zeros, so that it cannot spread.
  */

@@ -858,12 +858,12 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   const int group = q_heads / kv_heads;
   const int64_t rows = max_query * group;
   const int cap = kRowLimit;
-  // steps of the whole call: row blocks are bounded by the queries that there
-  // are; the longest line is the prefill form's with 64-key tiles
+  // The lines of both forms fit 32 bits: row blocks are bounded by the queries
+  // that there are, and an item takes its steps or tiles and what it costs besides.
   const int64_t keys = (int64_t)max_pages * page_size;
   const int64_t steps_max = (keys + kStep - 1) / kStep;
   const int64_t blocks = tokens * group / 128 + batch;
-  if ((int64_t)batch * kv_heads * (steps_max + kItemSteps) > 0x3FFFFFFF || blocks * kv_heads * (keys / 64 + 1) > 0x3FFFFFFF ||
+  if ((int64_t)batch * kv_heads * (steps_max + kItemSteps) > 0x3FFFFFFF || blocks * kv_heads * (keys / 64 + 4) > 0x3FFFFFFF ||
       (int64_t)batch * ((rows + 127) / 128) > 0x3FFFFFFF)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   DecodeArgs p = {};

@@ -48,10 +48,11 @@
 //    a proxy fence, or the next bulk copy passes reads that are still in flight.
 //
 // Measured, all three kernels: 4096 queries of 32 heads on 8 of 128 over their own
-// keys: 232 us, 590 TFLOP/s (37 % of cuBLAS's bf16 rate), bound by the chain S ->
-// exp2 -> P of a tile, whose exponentials alone take 1024 cycles of the SM, and by
-// what an item costs besides its tiles; 2048 queries of 32 heads on 4 of 256 over
-// 32 Ki keys: 2100 us, 1010 TFLOP/s (63 %), bound by shared-memory bandwidth:
+// keys: 217 us, 633 TFLOP/s (39 % of cuBLAS's bf16 rate), bound by the softmax
+// warps: of 2470 cycles a tile they spend 1500 in the weights (the exponentials
+// alone take 1024) and the rest waiting for S, loading it, voting and storing P;
+// an item costs about 13000 cycles besides.  2048 queries of 32 heads on 4 of 256
+// over 32 Ki keys: 2070 us, 1030 TFLOP/s (64 %), bound by shared-memory bandwidth:
 // 1500 us without the conversion and its stores.
 #include "attention.cuh"
 #include "attention_internal.cuh"
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       }
       // ---- the item's last P V, then O out, each thread half of its row.
       // (Q of the next item is loaded only behind it: held in registers meanwhile, it
-      // made the tile loop spill, 228 against 212 us for a prompt of 4096.)
+      // made the tile loop spill, 232 against 217 us for a prompt of 4096.)
       const bool whole = G.s0 == 0 && G.s1 == G.steps;
       const int64_t slot = 2 * (int64_t)blockIdx.x + kv::part_slot(blockIdx.x, walk.per, G.item_start);
       const int64_t at = (int64_t)(G.seq.first + qi) * A.heads_q + h;

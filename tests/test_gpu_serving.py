@@ -833,3 +833,31 @@ def test_norm_and_append_in_a_graph():
         assert torch.equal(qr, q2)
         for a in ("k_q", "k_sf", "v_q", "v_sf"):
             assert torch.equal(getattr(cache, a), getattr(other, a))
+
+
+def test_append_to_an_empty_pool_and_to_one_slot_twice():
+    """Without pages the queries are still turned; a slot named twice holds
+    finite values, and its neighbours are untouched."""
+    L = layer()
+    torch.manual_seed(2)
+    gs = torch.tensor([0.01], device="cuda")
+    k, v, q = (torch.randn(4, n, 64, device="cuda").to(torch.bfloat16) for n in (2, 2, 4))
+    rope, pos = L.rope_table(50, 64), torch.tensor([0, 9, 30, 49], device="cuda")
+    want = None
+    for pages, slots in ((0, [-1, -1, -1, -1]), (3, [7, 7, 20, 7])):
+        cache = L.PagedKVCache.empty(pages, 16, 2, 64, gs, gs)
+        for t in (cache.k_q, cache.k_sf, cache.v_q, cache.v_sf):
+            t.fill_(0x11)
+        st = status_word()
+        got = cache.append(k, v, torch.tensor(slots, device="cuda"), q=q, positions=pos, rope=rope, dev_status=st)
+        assert st.item() == 0
+        want = got if want is None else want
+        assert torch.equal(got, want)
+        if pages:
+            for t in (cache.k_q, cache.k_sf, cache.v_q, cache.v_sf):
+                rows = t.transpose(1, 2).reshape(pages * 16, -1)
+                keep = torch.ones(pages * 16, dtype=torch.bool, device="cuda")
+                keep[torch.tensor([7, 20], device="cuda")] = False
+                assert (rows[keep] == 0x11).all()
+            kd, vd = cache.dequantize()
+            assert torch.isfinite(kd).all() and torch.isfinite(vd).all()

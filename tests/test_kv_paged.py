@@ -199,6 +199,7 @@ APPEND_OK = dict(k=F, ld_k=512, v=F, ld_v=512, tokens=3, heads=4, D=128, slots=F
     (dict(ld_q=1016), nv.ERR_INVALID_ARG), (dict(qo=None), nv.ERR_INVALID_ARG), (dict(k=None), nv.ERR_INVALID_ARG),
     (dict(k=F + 8), nv.ERR_INVALID_ARG), (dict(slots=None), nv.ERR_INVALID_ARG), (dict(slots=F + 4), nv.ERR_INVALID_ARG),
     (dict(kgs=None), nv.ERR_INVALID_ARG), (dict(vq=None), nv.ERR_INVALID_ARG), (dict(kq=F + 8), nv.ERR_INVALID_ARG),
+    (dict(ks=F + 1), nv.ERR_INVALID_ARG), (dict(vs=F + 8), nv.ERR_INVALID_ARG),
     (dict(tokens=0, k=None, v=None, q=None), nv.OK)])
 def test_append_refusals(lib, change, want):
     assert _call(lib.nvfp4_kv_append, APPEND, APPEND_OK, **change) == want
