@@ -485,7 +485,9 @@ nvfp4_status nvfp4_kv_dequantize(const uint8_t *k_q, const uint8_t *k_sf, const 
  *  the dense MLP takes NVFP4 activations, the attention projections FP8 ones.]
  *   r = bf16(x + residual) (fp32 addition; r = x without a residual);
  *   y = bf16(r * weight / sqrt(mean(r^2) + eps)), the correctly rounded value
- *       (sum and root in 64 bits, one rounding);
+ *       (sum and root in 64 bits, one rounding) over bf16's whole range but its
+ *       lowest end: a y below 2^-100 max(1, |weight|) may be off by
+ *       2^-132 max(1, |weight|) before it is rounded;
  *   format BF16   y only.
  *   format NVFP4  q, sf = the bytes nvfp4_quantize writes for y in GIVEN mode.
  *   format E4M3   scale[row] = max(max|y| / 448, 2^-126) (1 for a zero row),

@@ -15,11 +15,15 @@
 // bytes per load.
 //
 // Rounding.  The sum of squares is kept in 64 bits (one conversion and one FMA
-// per element, which hide behind the loads) and 1/sqrt is one Newton step in 64
-// bits from the fp32 estimate (relative error below 2^-40); y is rounded to bf16
-// from an interval that holds it, or, where the interval's ends round apart, from
-// an unevaluated fp32 pair.  So y is the correctly rounded value, and the codes
-// behind it do not depend on the order of the sum.
+// per element) and 1/sqrt is one Newton step in 64 bits from the fp32 estimate
+// (relative error below 2^-40); y is rounded to bf16 from an interval that holds
+// it, or, where the interval's ends round apart, from an unevaluated fp32 pair.
+// So y is the correctly rounded value, and the codes behind it do not depend on
+// the order of the sum.  The root's power of two goes into r first, so that the
+// product with w leaves fp32's range only where y does; below 2^-100, or 2^-100 |w|,
+// what a subnormal drops makes y less exact.  (Such elements in 64 bits cost 270 to
+// 290 us instead of 217 for the large case: the test for them also finds the zeros
+// that a residual leaves, about one in 10^3.  Products as (r root) w: 223.)
 //
 // Measured with a residual, K 5120: 32768 rows to E4M3 215 us, 5.5 TB/s (84 % of a
 // copy's rate); 64 rows 6.2 us, which is one row's latency (load, two block
@@ -51,6 +55,12 @@ __device__ __forceinline__ uint32_t e4m3x2(float first, float second) {
   uint16_t out;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(second), "f"(first));
   return out;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 struct Args {
@@ -121,7 +131,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_rmsnorm_kernel(const Args
   } else {
     rs = 1.0 / sqrt(ms);                    // rows of values beyond 1e15 or below 1e-15
   }
+  const int e = max(-126, min(127, (int)((__double2hiint(rs) >> 20) & 0x7FF) - 1023));
+  rs *= __hiloint2double((1023 - e) << 20, 0);                 // in [1, 2), but for roots beyond 2^127 and zero rows
   const float rs_hi = (float)rs, rs_lo = (float)(rs - (double)rs_hi);
+  const uint32_t power = (uint32_t)(e + 127) << 7 | (uint32_t)(e + 127) << 23;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
@@ -136,10 +149,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_rmsnorm_kernel(const Args
       wa = __ldg(reinterpret_cast<const uint4 *>(A.w + 16 * j));
       wb = __ldg(reinterpret_cast<const uint4 *>(A.w + 16 * j + 8));
     }
-    // y = r w / sqrt(..): r * w is exact in fp32, and times the fp32 root it is off
-    // by less than 2^-23 of itself.  Where both ends of that interval round to
-    // the same bf16 -- for all but about one element in 2^12 -- that is y.
+    // y = r w / sqrt(..): r (with the root's power of two) times w is exact in fp32, and
+    // times the fp32 root it is off by less than 2^-23 of itself.  Where both ends of
+    // that interval round to the same bf16 -- for all but about one element in 2^12 --
+    // that is y.
     uint32_t yw[8], differ = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[i][k] = mul_bf16x2(r[i][k], power);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint64_t t = mul_f32x2(bf16x2_to_f32x2(r[i][k]), bf16x2_to_f32x2(word(wa, wb, k)));

@@ -1,0 +1,82 @@
+"""The serving operators at the ends of their ranges: values near the largest
+and smallest that bf16 holds, scores far apart, bad global scales, buffers used
+again, and batches that both forms of the attention share."""
+import numpy as np
+import pytest
+
+import oracle
+from tests._util import bf16_dev, to_dev, to_np
+from tests.test_gpu_serving import Case, bits_of, bf16_of, layer, nvmod, random_bf16, same, status_word, values
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_w4a4_quantized_04_b200 import build
+    build.build()
+
+
+def bf16_full(x):
+    """float64 -> the nearest bf16 (ties to even) as float64, subnormals and overflow included."""
+    _, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e - 8, -133))
+    r = np.rint(x / step) * step
+    return np.where(np.abs(r) >= 2.0 ** 128, np.copysign(np.inf, x), r)
+
+
+# ---------------------------------------------------------------------------------------- norm
+# r ~ 2^rows, w ~ 2^weights: the products r w leave fp32's range at either end while y is ordinary,
+# the root leaves it, or y itself is a subnormal
+@pytest.mark.parametrize("rows,weights,eps", [(126, 2, 1e-6), (120, 30, 1e-6), (100, 40, 1e-6), (126, 100, 0.0),
+                                              (-60, -80, 0.0), (-120, -20, 0.0), (-130, 0, 0.0), (-128, -126, 0.0),
+                                              (0, -127, 1e-6), (3, -131, 1e-6), (-80, 90, 1e-6), (-133, 30, 1e-30)])
+@pytest.mark.parametrize("K", [64, 5120, 20480])
+def test_norm_rounds_correctly_over_the_whole_range(rows, weights, eps, K):
+    """y is within 2^-40 of the exact value before its one rounding, so it is the
+    64-bit result's nearest bf16 unless that lies within 2^-40 of a border (about
+    2^-31 per element of a bf16 with 8 bits).  Below 2^-100 max(1, |w|) the
+    definition allows 2^-132 max(1, |w|) besides the rounding."""
+    L = layer()
+    rng = np.random.default_rng(1000 + rows + 7 * weights + K)
+    T = 5
+    x = bits_of(bf16_full(rng.uniform(1, 1.999, (T, K)) * rng.choice([-1, 1], (T, K)) * 2.0 ** rows))
+    x[1, ::3] = bits_of(bf16_full(values(x[1, ::3]) * 2.0 ** -9))     # elements far below their row's largest
+    x[2] = 0
+    w = bits_of(bf16_full(rng.uniform(1, 1.999, K) * 2.0 ** weights))
+    r = values(x)
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        y64 = r * values(w) / np.sqrt((r * r).mean(1, keepdims=True) + eps)
+    y = bf16_full(y64)
+    keep = [0, 1, 3, 4] + ([2] if eps else [])                        # 0 / 0 has no value
+    yd = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    st = status_word()
+    q, scale, _, _ = L.add_rmsnorm_e4m3(bf16_dev(x)[keep], bf16_dev(w), eps=eps, y=yd[:len(keep)], dev_status=st)
+    got = to_np(yd)[:len(keep)]
+    assert np.isfinite(y[keep]).all() and st.item() == 0
+    low = np.abs(y64[keep]) < 2.0 ** -100 * np.maximum(1.0, np.abs(values(w)))
+    same(np.where(low, 0.0, values(got)), np.where(low, 0.0, y[keep]))
+    half = np.ldexp(0.5, np.maximum(np.frexp(y64[keep])[1] - 8, -133))
+    assert (np.abs(values(got) - y64[keep]) <= half + 2.0 ** -132 * np.maximum(1.0, np.abs(values(w))))[low].all()
+    amax = np.abs(values(got)).max(1).astype(np.float32)
+    want = np.where(amax == 0, np.float32(1), np.maximum(amax / np.float32(448), np.float32(2.0 ** -126)))
+    same(to_np(scale), want)
+
+
+def test_norm_reports_what_overflows():
+    """A y beyond bf16's range is inf and reported; its neighbours in the row are not disturbed."""
+    L, nv = layer(), nvmod()
+    x = torch.ones(2, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    w[3] = 3.0e38
+    x[1, 3] = 8.0
+    y, st = torch.empty_like(x), status_word()
+    L.add_rmsnorm_e4m3(x[:1], w, y=y[:1], dev_status=st)
+    assert st.item() == 0 and torch.isfinite(y[0]).all()
+    L.add_rmsnorm_e4m3(x, w, y=y, dev_status=st)
+    assert st.item() == nv.ERR_NONFINITE and torch.isinf(y[1, 3]) and torch.isfinite(y[1, :3]).all()
+    assert torch.isfinite(y[0]).all()
