@@ -558,6 +558,7 @@ class PagedKVCache:
         _same_device(k_q, k_sf, k_gs, v_q, v_sf, v_gs)
         self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs = k_q, k_sf, k_gs, v_q, v_sf, v_gs
         self._need = {}                 # workspace bytes by (batch, max_query, q_heads)
+        self._captured = []             # workspaces that captured graphs point to
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, k_gs: torch.Tensor, v_gs: torch.Tensor,
@@ -614,7 +615,12 @@ class PagedKVCache:
         seq_lens int32 [batch]: cached tokens, the queries' own included;
         page_table int32 [batch, pages]; query_offsets int32 [batch + 1] (None:
         one query per sequence) with at most ``max_query`` queries each; lse:
-        fp32 [tokens, q_heads] to fill.  Returns out [tokens, q_heads, D]."""
+        fp32 [tokens, q_heads] to fill.  Returns out [tokens, q_heads, D].
+
+        ``ws`` (from ``workspace``; allocated when not given) serves one call at a
+        time.  One that is given to a captured call is kept as long as this cache:
+        a graph holds no reference to it, and a later capture's start gives
+        unused memory back to the device."""
         D = self.head_dim
         ld_q = _heads(q, None, D, "q")
         tokens, hq, _ = q.shape
@@ -638,13 +644,16 @@ class PagedKVCache:
         if need is None:
             need = self._need[batch, max_query, hq] = nvfp4_paged_attention_workspace_size(batch, max_query, hq,
                                                                                            self.heads, D)
-        if ws is None:
+        given = ws is not None
+        if not given:
             ws = self.k_q.new_empty(max(need, 1))
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
         _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws, dev_status)
         scale = D ** -0.5 if softmax_scale is None else softmax_scale
         with _on(self.k_q):
+            if given and torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured):
+                self._captured.append(ws)
             nvfp4_paged_attention(q, ld_q, tokens, query_offsets, max_query, seq_lens, batch, page_table,
                                   page_table.shape[1], hq, self.heads, D, self.k_q, self.k_sf, self.k_gs, self.v_q,
                                   self.v_sf, self.v_gs, self.num_pages, self.page_size, scale, int(causal), out,

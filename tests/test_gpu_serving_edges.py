@@ -1,6 +1,9 @@
 """The serving operators at the ends of their ranges: values near the largest
 and smallest that bf16 holds, scores far apart, bad global scales, buffers used
 again, and batches that both forms of the attention share."""
+import gc
+import weakref
+
 import numpy as np
 import pytest
 
@@ -80,3 +83,28 @@ def test_norm_reports_what_overflows():
     L.add_rmsnorm_e4m3(x, w, y=y, dev_status=st)
     assert st.item() == nv.ERR_NONFINITE and torch.isinf(y[1, 3]) and torch.isfinite(y[1, :3]).all()
     assert torch.isfinite(y[0]).all()
+
+
+# ---------------------------------------------------------------------------------------- attention
+def test_a_captured_workspace_outlives_its_last_reference():
+    """A graph points into the workspace; when the caller lets go of it, it must not
+    go back to the allocator, whose cache the next capture empties."""
+    c = Case(10, 256, 4, 8, 64, [3000, 500, 0], None, True)
+    want = c.run()
+    ws, out = c.cache.workspace(3, 1, 32), torch.zeros_like(c.q)
+    c.run(ws=ws, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(ws=ws, out=out)
+    held = weakref.ref(ws)
+    del ws
+    gc.collect()
+    assert held() is not None
+    y = torch.zeros(1, device="cuda")
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        y.add_(1)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
