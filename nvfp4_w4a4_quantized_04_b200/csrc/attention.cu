@@ -54,6 +54,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention.cuh"
 #include "attention_internal.cuh"
 #include "host_util.cuh"
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
       }
       uint32_t pb[2][NT][2];             // of the halves [kH] first
       float sum[NT][2];
-      auto take = [&]() {
+      auto take = [&](auto raised) {
         float most = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[h][k] = ex2(fmaf(s[h][nt][k], sc[nt][k & 1], -m[nt][k & 1]));
+            for (int k = 0; k < 4; ++k) p[h][k] = ex2(exponent<raised>(s[h][nt][k], sc[nt][k & 1], m[nt][k & 1]));
             pb[h][nt][0] = pack_f16x2(p[h][0], p[h][1]);
             pb[h][nt][1] = pack_f16x2(p[h][2], p[h][3]);
           }
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) sts_v2(p_mine + nt * 256, pb[0][nt][0], pb[0][nt][1]);
       };
-      bool raise = take();
+      bool raise = take(std::false_type{});
       if constexpr (kTeam == 1) {
         raise = __any_sync(0xffffffffu, raise);
       } else {
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
               o[j][nt][i + 2] *= f;
             }
           }
-        take();
+        take(std::true_type{});
         if constexpr (kTeam == 2) {
           turn();
           show();

@@ -20,6 +20,15 @@ __device__ __forceinline__ void row_power(int e, float &up, float &down) {
   down = plain ? 1.0f : __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
+// A score's exponent against the running maximum m.  Right after m was raised the
+// scaled score is rounded as m was, so that no weight exceeds 1: the fused form is
+// off from m by the rounding of m itself, which for scores beyond 2^27 is an
+// exponent that f16 does not hold.
+template <bool kRaised>
+__device__ __forceinline__ float exponent(float s, float sc, float m) {
+  return kRaised ? __fsub_rn(__fmul_rn(s, sc), m) : fmaf(s, sc, -m);
+}
+
 // Four output elements times f at (row `at`, element d).
 __device__ __forceinline__ void store_out(const Args &A, int64_t at, int D, int d, float4 acc, float f) {
   if (A.out_bf16) {

@@ -408,14 +408,18 @@ __device__ __forceinline__ void mask_scores(const Args &A, const Segment &G, uin
   }
 }
 
-// The weights exp2(s sc - m) of 64 scores as packed f16 pairs, and their fp32 sum.
+// The weights exp2(s sc - m) of 64 scores as packed f16 pairs, and their fp32 sum
+// (kRaised as in exponent()).
+template <bool kRaised>
 __device__ __forceinline__ float weights(const uint32_t (&s)[2][32], float sc, float m, uint32_t (&p)[32]) {
   const uint64_t sc2 = pair_f32(sc, sc), neg_m = pair_f32(-m, -m);
   uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     const uint32_t *x = &s[k >> 4][2 * (k & 15)];
-    const uint64_t v = fma_f32x2(((uint64_t)x[1] << 32) | x[0], sc2, neg_m);
+    // (the rounded form in scalars: a packed product and sum were fused all the same)
+    const uint64_t v = kRaised ? pair_f32(exponent<true>(__uint_as_float(x[0]), sc, m), exponent<true>(__uint_as_float(x[1]), sc, m))
+                               : fma_f32x2(((uint64_t)x[1] << 32) | x[0], sc2, neg_m);
     const float a = ex2(__uint_as_float((uint32_t)v)), b = ex2(__uint_as_float((uint32_t)(v >> 32)));
     if (k & 1) sum1 = add_f32x2(sum1, pair_f32(a, b));
     else sum0 = add_f32x2(sum0, pair_f32(a, b));
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
         if (__any_sync(0xffffffffu, limit - tok0 < 64) || bad) mask_scores(A, G, s, limit - tok0, tok0, bad);
         uint32_t p[32];
         float sum = 0.0f;
-        if (i > 0) sum = weights(s, sc, m, p);
+        if (i > 0) sum = weights<false>(s, sc, m, p);
         // Do the weights of any of the 32 rows call for larger maxima?
         if (pair_any(quad, i == 0 || sum > kMostSum)) {
           float top = __uint_as_float(s[0][0]);
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
             }
             tm_wait_st();
           }
-          sum = weights(s, sc, m, p);
+          sum = weights<true>(s, sc, m, p);
         }
         l += sum;
         // ---- P for the MMA.  The one tile in shared memory is free once P V of the

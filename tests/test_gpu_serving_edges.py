@@ -108,3 +108,40 @@ def test_a_captured_workspace_outlives_its_last_reference():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def one_key_case(D, queries, at, seed=4, hkv=2, group=4, n=700):
+    """A case whose queries look at one element only, in which token `at` has the
+    largest key of every head (72 times the head's scale; the others at most 20)."""
+    c = Case(seed, D, hkv, group, 64, [n], queries, True)
+    page, row = c.pages[0][at // 64], at % 64
+    c.t["k_sf"][c.t["k_sf"] == 0] = 0x38
+    c.t["k_sf"][page, :, row, 0] = 0x54                        # 12
+    c.t["k_q"][page, :, row, 0] = 0x77                         # 6, 6
+    c.t["k_q"][:, :, :, 0] &= 0x77                             # the element itself is not negative
+    return c
+
+
+def one_hot_queries(c, value):
+    q = torch.zeros_like(c.q)
+    q[..., 0] = value
+    return q
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("queries", [None, [4], [40]])
+@pytest.mark.parametrize("power", [12, 24, 27, 30, 60, 110])
+def test_attention_scores_far_apart_give_the_largest_keys_value(D, queries, power):
+    """Scores up to 2^118, beyond what fp32 resolves to units: the weights of all
+    keys but one vanish, and the output is that key's value.  Its weight is rounded
+    to f16 (2^-11) and the output to fp32."""
+    L = layer()
+    for at in (0, 333, 660):
+        c = one_key_case(D, queries, at)
+        q = one_hot_queries(c, 2.0 ** power)
+        want, lse, mag = c.reference(q=q)
+        ls = torch.zeros(c.q.shape[:2], device="cuda")
+        out = c.run(q=q, out_dtype=L.OUT_F32, lse=ls)
+        assert torch.isfinite(out).all()
+        assert ((out.double() - want).abs() <= mag * (2.0 ** -11 + 2.0 ** -22)).all()
+        assert ((ls - lse).abs() <= 2.0 ** -21 * lse.abs()).all()
