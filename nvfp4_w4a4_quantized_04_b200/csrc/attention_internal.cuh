@@ -8,7 +8,7 @@
 namespace nvfp4 {
 namespace attn {
 
-constexpr float kFloor = -1e30f;         // running maximum before the first key
+constexpr float kFloor = -3.40282347e38f; // running maximum before the first key: the lowest fp32, below any score
 constexpr int kMaxBatch = 4096;
 
 // The power of two that brings a row of Q to f16: 2^(14 - e) for a row whose

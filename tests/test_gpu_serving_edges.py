@@ -145,3 +145,24 @@ def test_attention_scores_far_apart_give_the_largest_keys_value(D, queries, powe
         assert torch.isfinite(out).all()
         assert ((out.double() - want).abs() <= mag * (2.0 ** -11 + 2.0 ** -22)).all()
         assert ((ls - lse).abs() <= 2.0 ** -21 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("queries", [None, [4], [40]])
+@pytest.mark.parametrize("power", [60, 110, 122])
+def test_attention_scores_all_far_below_zero(D, queries, power):
+    """All of a row's scores at -2^57 to -2^122: the least negative one wins, and the
+    row is neither zeros nor without a sum.  Tolerances as above."""
+    L = layer()
+    for at in (0, 333, 660):
+        c = one_key_case(D, queries, at)
+        page, row = c.pages[0][at // 64], at % 64
+        c.t["k_q"][:, :, :, 0] = 0x22                              # 1, 1
+        c.t["k_sf"][:, :, :, 0] = 0x38                             # 1
+        c.t["k_sf"][page, :, row, 0] = 0x30                        # 0.5
+        q = one_hot_queries(c, -(2.0 ** power))
+        want, lse, mag = c.reference(q=q)
+        ls = torch.zeros(c.q.shape[:2], device="cuda")
+        out = c.run(q=q, out_dtype=L.OUT_F32, lse=ls)
+        assert ((out.double() - want).abs() <= mag * (2.0 ** -11 + 2.0 ** -22)).all()
+        assert ((ls - lse).abs() <= 2.0 ** -21 * lse.abs()).all()
