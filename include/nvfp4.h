@@ -583,6 +583,8 @@ nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void *v, int64_t
  *   causal         1: with n queries and length L, query j sees keys
  *                  [0, L - n + j]; 0: all L.  A query that sees none gives a row
  *                  of zeros (lse -inf).
+ *   k_gs, v_gs     fp32 [1], finite and > 0: another value is reported as
+ *                  NVFP4_ERR_INVALID_ARG, and rows that see keys come out as NaN.
  *   head_dim       64, 128 or 256; q_heads a multiple of kv_heads; batch <= 4096.
  *   out            fp32 or bf16 [tokens, q_heads, head_dim], 16-byte aligned.
  *                  Rows outside every sequence's queries are left as they were.

@@ -230,7 +230,9 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
       if (A.lse && i % (D / 4) == 0) A.lse[at] = -INFINITY;
     }
   }
-  const float kgs = __ldg(A.k_gs), vgs = __ldg(A.v_gs);
+  const bool scales = scales_ok(A);
+  if (!scales && blockIdx.x == 0 && tid == 0) report(A.dev_status, NVFP4_ERR_INVALID_ARG);
+  const float kgs = scales ? __ldg(A.k_gs) : NAN, vgs = __ldg(A.v_gs);
   int pos = (int)min((int64_t)total, (int64_t)blockIdx.x * per_cta);
   const int end = (int)min((int64_t)total, (int64_t)pos + per_cta);
   const uint32_t ring = smem_addr(smem) + team * kStages * L::kStageBytes;
@@ -296,9 +298,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) decode_kernel(const Dec
         else
           *reinterpret_cast<uint32_t *>(dst) = pack_f16x2(v[i] * up, v[i + 1] * up);
       }
-      // never 0, so that a masked score of -inf stays -inf
-      if (lane == 0)
-        s_row[r] = make_float2(fmaxf(A.scale_log2 * kgs * kScaleFix * down, 1.17549435e-38f), __int_as_float(limit));
+      if (lane == 0) s_row[r] = make_float2(score_scale(A, kgs, down), __int_as_float(limit));
     }
     __syncthreads();
     float sc[NT][2];

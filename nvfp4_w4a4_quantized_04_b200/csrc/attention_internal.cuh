@@ -20,6 +20,18 @@ __device__ __forceinline__ void row_power(int e, float &up, float &down) {
   down = plain ? 1.0f : __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
+// Both global scales finite and above 0.
+__device__ __forceinline__ bool scales_ok(const Args &A) {
+  const float k = __ldg(A.k_gs), v = __ldg(A.v_gs);
+  return k > 0.0f && k <= 3.40282347e38f && v > 0.0f && v <= 3.40282347e38f;
+}
+// The factor from a row's f16 score to log2 units.  Never 0, so that a masked score
+// of -inf stays -inf; NaN with a bad global scale, so that it shows in the output.
+__device__ __forceinline__ float score_scale(const Args &A, float k_gs, float down) {
+  const float x = A.scale_log2 * k_gs * kScaleFix * down;
+  return x < 1.17549435e-38f ? 1.17549435e-38f : x;
+}
+
 // A score's exponent against the running maximum m.  Right after m was raised the
 // scaled score is rounded as m was, so that no weight exceeds 1: the fused form is
 // off from m by the rounding of m itself, which for scores beyond 2^27 is an

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Args &A = P.a;
   const int t = threadIdx.x;
+  if (t == 0 && !scales_ok(A)) report(A.dev_status, NVFP4_ERR_INVALID_ARG);
   bool bad = false;
   for (int b = t; b < A.batch; b += kPlanThreads) bad |= !offsets_ok(A, b);
   if (__syncthreads_or(bad)) {
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const int r = 32 * quad + lane;                       // row of the block
     volatile float *xch = reinterpret_cast<volatile float *>(smem + L::kXch);
-    const float kgs = __ldg(A.k_gs), vgs = __ldg(A.v_gs);
+    const float kgs = scales_ok(A) ? __ldg(A.k_gs) : NAN, vgs = __ldg(A.v_gs);
     uint32_t tile = 0, item = 0;
     // A wait that gives up (abort) does not end the loop: the two warps of a row
     // stay in step, every later wait returns at once, and nothing more is stored.
@@ -747,8 +748,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const PlanArgs 
       tm_wait_st();
       tc_fence_before();
       mbar_arrive(q_ready);
-      // never 0, so that a masked score of -inf stays -inf
-      const float sc = fmaxf(A.scale_log2 * kgs * kScaleFix * down, 1.17549435e-38f);
+      const float sc = score_scale(A, kgs, down);
       const int limit = live ? (int)kv::visible_keys(G.seq.len, G.seq.queries, qi, A.causal != 0) : 0;
       float m = kFloor, l = 0.0f;
       const int n = G.s1 - G.s0;

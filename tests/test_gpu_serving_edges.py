@@ -166,3 +166,27 @@ def test_attention_scores_all_far_below_zero(D, queries, power):
         out = c.run(q=q, out_dtype=L.OUT_F32, lse=ls)
         assert ((out.double() - want).abs() <= mag * (2.0 ** -11 + 2.0 ** -22)).all()
         assert ((ls - lse).abs() <= 2.0 ** -21 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("queries", [None, [4, 3], [40, 1]])
+def test_attention_reports_bad_global_scales(D, queries):
+    """A scale of zero, below it, NaN or inf is reported, and the outputs are NaN
+    rather than a plausible average of the values."""
+    L, nv = layer(), nvmod()
+    c = Case(12, D, 2, 4, 64, [200, 70], queries, True)
+    good = c.run()
+    for bad in (0.0, -0.5, float("nan"), float("inf")):
+        for which in ("k_gs", "v_gs"):
+            keep = getattr(c.cache, which)
+            setattr(c.cache, which, torch.tensor([bad], device="cuda"))
+            st = status_word()
+            out = c.run(out_dtype=L.OUT_F32, dev_status=st)
+            setattr(c.cache, which, keep)
+            assert st.item() == nv.ERR_INVALID_ARG and torch.isnan(out).all()
+    st = status_word()
+    assert torch.equal(c.run(dev_status=st), good) and st.item() == 0
+    # one so small that the scaled score is a subnormal is still good
+    c.cache.k_gs = torch.tensor([1e-44], device="cuda")
+    out = c.run(out_dtype=L.OUT_F32, dev_status=st)
+    assert st.item() == 0 and torch.isfinite(out).all()
