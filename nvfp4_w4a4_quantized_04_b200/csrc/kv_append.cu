@@ -51,22 +51,22 @@ __device__ __forceinline__ float half_f32(uint32_t w, int h) {
   return h ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
 }
 
-// bf16(a c - b s), rounded once: both products with their errors.
+// bf16(a c - b s), rounded once, in 64 bits: the products are exact there, their sum is
+// truncated, and what it and the step to fp32 drop goes into the last bit.
 __device__ __forceinline__ uint32_t rot_bf16(float a, float c, float b, float s) {
-  const float p = __fmul_rn(a, c), e = __fmaf_rn(a, c, -p);
-  const float q = __fmul_rn(b, s), f = __fmaf_rn(b, s, -q);
-  const float hi = __fsub_rn(p, q);
-  const float v = __fsub_rn(hi, p);
-  const float t = __fsub_rn(__fsub_rn(p, __fsub_rn(hi, v)), __fadd_rn(q, v));
-  return bf16_of_sum(hi, __fadd_rn(t, __fsub_rn(e, f)));
+  const double q = (double)b * (double)s, z = __fma_rz((double)a, (double)c, -q);
+  const float f = __double2float_rz(z);
+  const bool dropped = (double)f != z || __fma_ru((double)a, (double)c, -q) != __fma_rd((double)a, (double)c, -q);
+  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(__float_as_uint(f) | (dropped ? 1u : 0u))));
 }
 
 // The same for the usual element: q = b s and r = fma(a, c, -q) are off by less
-// than 2^-23 (|q| + |r|); where both ends of a wider interval round to the same
-// bf16 (all but about one element in 2^12), `lo` and `hi` agree.
+// than 2^-23 (|q| + |r|) and, as subnormals, 2^-149; where both ends of a wider
+// interval round to the same bf16 (all but about one element in 2^12, and those below
+// 2^-140), `lo` and `hi` agree.
 __device__ __forceinline__ void rot_interval(float a, float c, float b, float s, float &lo, float &hi) {
   const float q = __fmul_rn(b, s), r = __fmaf_rn(a, c, -q);
-  const float e = fabsf(q) + fabsf(r);
+  const float e = fabsf(q) + 0x1p-118f + fabsf(r);
   lo = __fmaf_rn(e, -0x1p-22f, r);
   hi = __fmaf_rn(e, 0x1p-22f, r);
 }

@@ -190,3 +190,49 @@ def test_attention_reports_bad_global_scales(D, queries):
     c.cache.k_gs = torch.tensor([1e-44], device="cuda")
     out = c.run(out_dtype=L.OUT_F32, dev_status=st)
     assert st.item() == 0 and torch.isfinite(out).all()
+
+
+# ---------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("power,gain", [(-133, 1.0), (-128, 1.0), (-126, 1.0), (-110, 2.0 ** -20), (0, 2.0 ** -126),
+                                        (120, 1.0), (127, 1.0), (126, 3.0), (100, 2.0 ** 30), (0, 1.0)])
+def test_append_rounds_correctly_over_the_whole_range(power, gain, pairs):
+    """Rotated queries and keys are the 64-bit result's nearest bf16, for values and
+    tables whose products are subnormal in fp32 or leave its range (the products are
+    exact in 64 bits, their sum is off by 2^-53, so that another bf16 would need a
+    border within that)."""
+    L = layer()
+    rng = np.random.default_rng(2000 + power + int(pairs))
+    T, heads, D, rot = 1000, 2, 64, 64
+    with np.errstate(over="ignore"):
+        x = bits_of(bf16_full(rng.standard_normal((T, heads, D)) * 2.0 ** power))
+    x[np.isinf(values(x))] = 0x7F7F
+    x[:40] = 0
+    x[40:80, :, ::2] = 0
+    pos = rng.integers(0, 5000, T).astype(np.int64)
+    pos[:100] = 0
+    table = L.rope_table(5000, rot) * gain
+    tab = table.double().cpu().numpy()
+    c, s = tab[pos, None, :rot // 2], tab[pos, None, rot // 2:]
+    v, want = values(x), np.empty((T, heads, D))
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if pairs else (slice(0, rot // 2), slice(rot // 2, rot))
+    want[..., a] = v[..., a] * c - v[..., b] * s
+    want[..., b] = v[..., b] * c + v[..., a] * s
+    with np.errstate(over="ignore"):
+        want = bf16_full(want)
+    gs = np.float32(min(max(2.0 ** power * gain / 300, 2.0 ** -100), 2.0 ** 100))
+    g = torch.tensor([gs], device="cuda")
+    cache = L.PagedKVCache.empty(63, 16, heads, D, g, g)
+    st = status_word()
+    xd = bf16_dev(x)
+    got = cache.append(xd, xd, torch.arange(T, device="cuda"), q=xd, positions=to_dev(pos), rope=table, interleaved=pairs,
+                       dev_status=st)
+    same(values(to_np(got)), want)
+    finite = np.isfinite(want)
+    assert st.item() == (0 if finite.all() else nvmod().ERR_NONFINITE)
+    blocks = finite.reshape(T, heads, D // 16, 16).all(-1)
+    q_, sf_, _ = oracle.quantize(bits_of(np.where(finite, want, 0.0)).reshape(T * heads, D), global_scale=np.array([gs], np.float32))[:3]
+    kq = to_np(cache.k_q.transpose(1, 2).reshape(-1, heads, D // 2)[:T].contiguous()).reshape(T, heads, D // 16, 8)
+    ks = to_np(cache.k_sf.transpose(1, 2).reshape(-1, heads, D // 16)[:T].contiguous())
+    same(kq, np.where(blocks[..., None], q_.reshape(T, heads, D // 16, 8), np.uint8(0)))
+    same(ks, np.where(blocks, sf_.reshape(T, heads, D // 16), np.uint8(0)))
