@@ -32,7 +32,8 @@ class Packed:
 
     q: uint8 [rows_alloc, K/2]; sf: uint8 scales (``layout``); gs: fp32 [G]
     global scales.  With ``offsets`` (int32 [G+1] on the device) rows sit in
-    128-aligned per-group slots.
+    128-aligned per-group slots.  ``gs_given``: gs is a tensor of the caller's (a
+    calibrated scale); quantizing into this Packed again gives it scales of its own.
     """
     q: torch.Tensor
     sf: torch.Tensor
@@ -42,6 +43,15 @@ class Packed:
     layout: int
     offsets: Optional[torch.Tensor] = None
     num_groups: int = 1
+    gs_given: bool = False
+
+
+def _own_scales(p: Packed, G: int):
+    """Make p.gs a tensor that a call may write G scales to."""
+    if p.gs_given:
+        p.gs, p.gs_given = torch.empty(max(1, G), dtype=torch.float32, device=p.q.device), False
+    elif p.gs.numel() < G:
+        raise ValueError(f"out: {G} global scales are wanted, not {p.gs.numel()}")
 
 
 def workspace(num_groups: int, device="cuda") -> torch.Tensor:
@@ -76,6 +86,7 @@ def quantize(x: torch.Tensor, row_index=None, offsets=None, num_groups: int = 1,
     R = rows if rows is not None else (row_index.shape[0] if row_index is not None else x.shape[0])
     G = num_groups if offsets is not None else 1
     p = out if out is not None else empty_packed(R, K, G, offsets, layout, x.device)
+    _own_scales(p, G)
     p.offsets, p.num_groups, p.rows = offsets, G, R
     mode = GS_FROM_AMAX
     if global_scale is not None:
@@ -96,6 +107,7 @@ def moe_quantize(x: torch.Tensor, slot: torch.Tensor, offsets: torch.Tensor, num
     K = x.shape[1]
     R = rows if rows is not None else T * k
     p = out if out is not None else empty_packed(R, K, num_groups, offsets, layout, x.device)
+    _own_scales(p, num_groups)
     p.offsets, p.num_groups, p.rows = offsets, num_groups, R
     ws = ws if ws is not None else workspace(num_groups, x.device)
     nvfp4_moe_quantize(x, T, K, x.stride(0), slot, k, offsets, num_groups, GS_FROM_AMAX, p.gs, p.q, p.sf, layout,
@@ -208,7 +220,7 @@ def grouped_gemm_swiglu_nvfp4(a: Packed, w_gate_up: Packed, N: int, h_gs: torch.
     I = N // 2
     p = out if out is not None else empty_packed(a.rows, I, E, a.offsets, SF_MMA_TILED, a.q.device)
     p.offsets, p.num_groups, p.rows = a.offsets, E, a.rows
-    p.gs = h_gs
+    p.gs, p.gs_given = h_gs, True
     nvfp4_grouped_gemm_swiglu_nvfp4(a.q, a.sf, a.gs, w_gate_up.q, w_gate_up.sf, w_gate_up.gs, a.offsets, E, a.rows,
                                     N, a.K, h_gs, p.q, p.sf, None, dev_status)
     return p
@@ -242,6 +254,7 @@ def swiglu_quantize(y: torch.Tensor, offsets, num_groups: int, layout=SF_MMA_TIL
     I = I2 // 2
     G = num_groups if offsets is not None else 1
     p = out if out is not None else empty_packed(rows, I, G, offsets, layout, y.device)
+    _own_scales(p, G)
     p.offsets, p.num_groups, p.rows = offsets, G, rows
     h = h if h is not None else torch.empty((rows, I), dtype=torch.bfloat16, device=y.device)
     ws = ws if ws is not None else workspace(G, y.device)
@@ -473,9 +486,9 @@ def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch
     """r = x + residual, y = rmsnorm(r) * weight, and y as NVFP4 with the given
     global scale (a calibrated ``input_scale``, fp32 [1]), in one pass.
 
-    Returns (packed y, r, y): r is ``residual_out`` (allocated when a residual
-    is given; may be ``residual`` itself) or x; y is the bf16 buffer passed as
-    ``y``, or None."""
+    Returns (packed y, r, y): the packed y holds ``global_scale`` itself (no copy);
+    r is ``residual_out`` (allocated when a residual is given; may be ``residual``
+    itself) or x; y is the bf16 buffer passed as ``y``, or None."""
     rows, K, ld_x, ld_res, residual_out, ld_ro = _norm_args(x, weight, residual, residual_out)
     if global_scale.dtype != torch.float32 or global_scale.numel() != 1:
         raise ValueError("global_scale: an fp32 tensor of one element is wanted")
@@ -487,7 +500,7 @@ def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch
     if p.sf.numel() < sf_bytes(alloc_rows(rows, 1, False, layout), K):
         raise ValueError("out: too few bytes of scales")
     _same_device(x, global_scale, y, p.q, p.sf, dev_status)
-    p.gs, p.offsets, p.num_groups, p.rows = global_scale, None, 1, rows
+    p.gs, p.gs_given, p.offsets, p.num_groups, p.rows = global_scale, True, None, 1, rows
     with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
                                    NORM_NVFP4, global_scale, p.q, p.sf, layout, dev_status)

@@ -1,0 +1,88 @@
+"""The host side of the serving operators: which buffers a call writes through, and
+what the layer refuses before a kernel could run.  CPU only: the library's calls are
+recorded instead of made."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from nvfp4_w4a4_quantized_04_b200 import layer as L  # noqa: E402
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's entry points replaced by a record of their arguments."""
+    seen = []
+
+    def fake(name):
+        return lambda *a, **k: seen.append((name, a))
+    for name in ("nvfp4_quantize", "nvfp4_moe_quantize", "nvfp4_swiglu_quantize", "nvfp4_add_rmsnorm_quantize",
+                 "nvfp4_kv_append", "nvfp4_paged_attention", "nvfp4_grouped_gemm_swiglu_nvfp4"):
+        monkeypatch.setattr(L, name, fake(name))
+    monkeypatch.setattr(L, "_on", lambda t: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return seen
+
+
+def bf16(*shape):
+    return torch.ones(shape, dtype=torch.bfloat16)
+
+
+# where each entry point gets the global scales that it writes
+GS = {"nvfp4_quantize": 8, "nvfp4_moe_quantize": 9, "nvfp4_swiglu_quantize": 6}
+
+
+@pytest.mark.parametrize("again", ["quantize", "given", "grouped", "moe", "swiglu"])
+def test_a_reused_output_never_writes_through_the_callers_scale(calls, again):
+    """add_rmsnorm_nvfp4's output holds the model's calibrated scale.  A later
+    quantization into the same buffers has scales of its own, one per group."""
+    E, K = 4, 64
+    scale = torch.full((1,), 0.25)
+    offsets = torch.arange(0, E + 1, dtype=torch.int32) * 2
+    p = L.empty_packed(8, K, E, offsets, device="cpu")
+    got, _, _ = L.add_rmsnorm_nvfp4(bf16(8, K), bf16(K), scale, out=p)
+    assert got is p and p.gs is scale
+    if again == "quantize":
+        L.quantize(bf16(8, K), out=p)
+    elif again == "given":
+        L.quantize(bf16(8, K), out=p, global_scale=torch.full((1,), 3.0))
+        assert p.gs[0] == 3.0
+    elif again == "grouped":
+        L.quantize(bf16(8, K), offsets=offsets, num_groups=E, out=p)
+    elif again == "moe":
+        L.moe_quantize(bf16(8, K), torch.zeros(8, 1, dtype=torch.int32), offsets, E, out=p)
+    else:
+        L.swiglu_quantize(bf16(8, 2 * K), offsets, E, out=p)
+    name, args = calls[-1]
+    written = args[GS[name]]
+    assert written.data_ptr() != scale.data_ptr() and scale[0] == 0.25
+    assert written.numel() >= (1 if again in ("quantize", "given") else E) and written is p.gs
+    # and the buffers serve the norm again
+    L.add_rmsnorm_nvfp4(bf16(8, K), bf16(K), scale, out=p)
+    assert p.gs is scale and scale[0] == 0.25
+
+
+def test_an_output_with_too_few_scales_is_refused(calls):
+    E, K = 4, 64
+    offsets = torch.arange(0, E + 1, dtype=torch.int32) * 2
+    p = L.empty_packed(8, K, E, offsets, device="cpu")
+    p.gs = torch.empty(E - 1)
+    for call in (lambda: L.quantize(bf16(8, K), offsets=offsets, num_groups=E, out=p),
+                 lambda: L.moe_quantize(bf16(8, K), torch.zeros(8, 1, dtype=torch.int32), offsets, E, out=p),
+                 lambda: L.swiglu_quantize(bf16(8, 2 * K), offsets, E, out=p)):
+        with pytest.raises(ValueError, match="global scales"):
+            call()
+    assert not calls
+
+
+def test_the_calibrated_scale_of_the_experts_is_not_written(calls):
+    """grouped_gemm_swiglu_nvfp4's output holds the given scales, too."""
+    E, K = 2, 64
+    offsets = torch.arange(0, E + 1, dtype=torch.int32) * 4
+    a = L.empty_packed(8, K, E, offsets, device="cpu")
+    h_gs = torch.full((E,), 0.5)
+    p = L.grouped_gemm_swiglu_nvfp4(a, L.empty_packed(2 * K * E, K, device="cpu"), 2 * K, h_gs)
+    assert p.gs is h_gs
+    L.swiglu_quantize(bf16(8, 2 * K), offsets, E, out=p)
+    assert calls[-1][1][GS["nvfp4_swiglu_quantize"]].data_ptr() != h_gs.data_ptr()
