@@ -621,14 +621,16 @@ class PagedKVCache:
         n = nvfp4_paged_attention_workspace_size(batch, max_query, q_heads, self.heads, self.head_dim)
         return torch.empty(max(n, 1), dtype=torch.uint8, device=self.k_q.device)
 
-    def attend(self, q, seq_lens, page_table, query_offsets=None, max_query: int = 1, softmax_scale=None,
+    def attend(self, q, seq_lens, page_table, query_offsets=None, max_query: Optional[int] = None, softmax_scale=None,
                causal: bool = True, out=None, out_dtype=OUT_BF16, lse=None, ws=None, dev_status=None):
         """Attention of q (bf16 [tokens, q_heads, D]) over the cache.
 
         seq_lens int32 [batch]: cached tokens, the queries' own included;
-        page_table int32 [batch, pages]; query_offsets int32 [batch + 1] (None:
-        one query per sequence) with at most ``max_query`` queries each; lse:
-        fp32 [tokens, q_heads] to fill.  Returns out [tokens, q_heads, D].
+        page_table int32 [batch, pages]; query_offsets int32 [batch + 1] with at
+        most ``max_query`` queries each, which has to be given with them (None:
+        one query per sequence); lse: fp32 [tokens, q_heads] to fill.  Returns
+        out [tokens, q_heads, D].  Offsets that break this are reported in
+        ``dev_status`` and nothing is computed.
 
         ``ws`` (from ``workspace``; allocated when not given) serves one call at a
         time.  One that is given to a captured call is kept as long as this cache:
@@ -646,6 +648,12 @@ class PagedKVCache:
         if query_offsets is not None and (query_offsets.dtype != torch.int32 or query_offsets.shape != (batch + 1,) or
                                           not query_offsets.is_contiguous()):
             raise ValueError("query_offsets: a contiguous int32 [batch + 1] tensor is wanted")
+        if query_offsets is None:
+            if max_query not in (None, 1):
+                raise ValueError("max_query: one query per sequence without query_offsets")
+            max_query = 1
+        elif max_query is None:
+            raise ValueError("max_query: the most queries of a sequence is wanted with query_offsets")
         dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
         if out is None:
             out = torch.empty_like(q, dtype=dt, memory_format=torch.contiguous_format)

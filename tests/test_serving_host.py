@@ -86,3 +86,33 @@ def test_the_calibrated_scale_of_the_experts_is_not_written(calls):
     assert p.gs is h_gs
     L.swiglu_quantize(bf16(8, 2 * K), offsets, E, out=p)
     assert calls[-1][1][GS["nvfp4_swiglu_quantize"]].data_ptr() != h_gs.data_ptr()
+
+
+# ---------------------------------------------------------------------------------------- attention
+def cache(pages=4, heads=2, ps=16, D=64):
+    def u8(*s):
+        return torch.zeros(s, dtype=torch.uint8)
+    gs = torch.ones(1)
+    return L.PagedKVCache(u8(pages, heads, ps, D // 2), u8(pages, heads, ps, D // 16), gs,
+                          u8(pages, heads, ps, D // 2), u8(pages, heads, ps, D // 16), gs)
+
+
+def attend_args(counts=(3, 2), D=64):
+    offsets = torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32)
+    return dict(q=bf16(sum(counts), 4, D), seq_lens=torch.full((2,), 9, dtype=torch.int32),
+                page_table=torch.zeros(2, 2, dtype=torch.int32), query_offsets=offsets)
+
+
+def test_query_offsets_without_max_query_are_refused(calls):
+    """The kernels compute nothing for a sequence of more queries than max_query, so
+    that a forgotten one would return memory as it was found."""
+    a = attend_args()
+    with pytest.raises(ValueError, match="max_query"):
+        cache().attend(**a)
+    assert not calls
+    cache().attend(**a, max_query=3)
+    cache().attend(**a, max_query=1)                 # said so: at most one each (the device reports it)
+    cache().attend(a["q"][:2], a["seq_lens"], a["page_table"])
+    assert [c[1][4] for c in calls] == [3, 1, 1]
+    with pytest.raises(ValueError, match="max_query"):
+        cache().attend(a["q"][:2], a["seq_lens"], a["page_table"], max_query=2)
