@@ -468,6 +468,12 @@ def _same_device(first, *others):
             raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
+def _status(t):
+    """A status word for the device to write, or None."""
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise ValueError("dev_status: an int32 tensor of one element is wanted")
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -495,10 +501,13 @@ def add_rmsnorm_nvfp4(x: torch.Tensor, weight: torch.Tensor, global_scale: torch
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
         raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
     p = out if out is not None else empty_packed(rows, K, 1, None, layout, x.device)
-    if p.K != K or p.layout != layout or p.q.shape[0] < alloc_rows(rows, 1, False, layout):
-        raise ValueError("out: a packed tensor of this K and layout with enough rows is wanted")
-    if p.sf.numel() < sf_bytes(alloc_rows(rows, 1, False, layout), K):
-        raise ValueError("out: too few bytes of scales")
+    ra = alloc_rows(rows, 1, False, layout)
+    if p.K != K or p.layout != layout or p.q.dim() != 2 or p.q.shape[0] < ra or p.q.shape[1] != K // 2 or \
+            p.q.dtype != torch.uint8 or not p.q.is_contiguous():
+        raise ValueError("out: packed uint8 codes of this K and layout with enough rows are wanted")
+    if p.sf.dtype != torch.uint8 or not p.sf.is_contiguous() or p.sf.numel() < sf_bytes(ra, K):
+        raise ValueError("out: uint8 scales, enough of them, are wanted")
+    _status(dev_status)
     _same_device(x, global_scale, y, p.q, p.sf, dev_status)
     p.gs, p.gs_given, p.offsets, p.num_groups, p.rows = global_scale, True, None, 1, rows
     with _on(x):
@@ -522,6 +531,7 @@ def add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: 
         raise ValueError("scale: fp32 [rows] is wanted")
     if y is not None and (y.dtype != torch.bfloat16 or y.shape != x.shape or not y.is_contiguous()):
         raise ValueError("y: a contiguous bf16 tensor of x's shape is wanted")
+    _status(dev_status)
     _same_device(x, q, scale, y, dev_status)
     with _on(x):
         nvfp4_add_rmsnorm_quantize(x, ld_x, residual, ld_res, rows, K, weight, eps, residual_out, ld_ro, y,
@@ -609,6 +619,7 @@ class PagedKVCache:
                 ld_qo = _heads(q_out, tokens, D, "q_out")
                 if q_out.shape != q.shape:
                     raise ValueError("q_out: the shape of q is wanted")
+        _status(dev_status)
         _same_device(self.k_q, k, v, slots, q, q_out, positions, rope, dev_status)
         with _on(self.k_q):
             nvfp4_kv_append(k, ld_k, v, ld_v, tokens, self.heads, D, slots, q, ld_q, hq, q_out, ld_qo, positions, rope,
@@ -668,8 +679,9 @@ class PagedKVCache:
         given = ws is not None
         if not given:
             ws = self.k_q.new_empty(max(need, 1))
-        elif ws.numel() * ws.element_size() < need:
-            raise ValueError("ws: too small (PagedKVCache.workspace gives one)")
+        elif ws.numel() * ws.element_size() < need or not ws.is_contiguous():
+            raise ValueError("ws: too small, or with gaps (PagedKVCache.workspace gives one)")
+        _status(dev_status)
         _same_device(self.k_q, q, seq_lens, page_table, query_offsets, out, lse, ws, dev_status)
         scale = D ** -0.5 if softmax_scale is None else softmax_scale
         with _on(self.k_q):

@@ -116,3 +116,36 @@ def test_query_offsets_without_max_query_are_refused(calls):
     assert [c[1][4] for c in calls] == [3, 1, 1]
     with pytest.raises(ValueError, match="max_query"):
         cache().attend(a["q"][:2], a["seq_lens"], a["page_table"], max_query=2)
+
+
+def test_buffers_that_a_kernel_would_leave_are_refused(calls):
+    """Workspaces and packed outputs with gaps, and status words that are not one 32-bit
+    integer at least: a kernel takes them for dense and would write behind their ends."""
+    a = attend_args()
+    a["max_query"] = 3
+    need = cache().workspace(2, 3, 4).numel()
+    gaps = torch.empty(2 * need, dtype=torch.uint8)[::2]
+    assert gaps.numel() >= need
+    with pytest.raises(ValueError, match="ws"):
+        cache().attend(**a, ws=gaps)
+    x, w, gs = bf16(4, 64), bf16(64), torch.ones(1)
+    kv = bf16(3, 2, 64)
+    slots = torch.zeros(3, dtype=torch.int64)
+    for bad in (torch.zeros(1, dtype=torch.int8), torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32)):
+        for call in (lambda: cache().attend(**a, dev_status=bad), lambda: cache().append(kv, kv, slots, dev_status=bad),
+                     lambda: L.add_rmsnorm_e4m3(x, w, dev_status=bad), lambda: L.add_rmsnorm_nvfp4(x, w, gs, dev_status=bad)):
+            with pytest.raises(ValueError, match="dev_status"):
+                call()
+    for name in ("q", "sf"):
+        p = L.empty_packed(4, 64, device="cpu")
+        t = getattr(p, name)
+        wide = torch.empty(*t.shape[:-1], 2 * t.shape[-1], dtype=torch.uint8)
+        for bad in (wide[..., ::2], t.view(torch.int8), t.float(), t[..., :t.shape[-1] // 2]):
+            setattr(p, name, bad)
+            with pytest.raises(ValueError, match="out"):
+                L.add_rmsnorm_nvfp4(x, w, gs, out=p)
+    assert not calls
+    ok = torch.zeros(2, dtype=torch.int32)
+    cache().attend(**a, ws=torch.empty(need, dtype=torch.uint8), dev_status=ok)
+    L.add_rmsnorm_nvfp4(x, w, gs, dev_status=ok)
+    assert len(calls) == 2
