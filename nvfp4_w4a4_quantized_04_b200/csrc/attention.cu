@@ -794,7 +794,10 @@ nvfp4_status run(DecodeArgs p, int64_t total_bound, uint8_t *ws, cudaStream_t st
   auto kern = decode_kernel<D, NT, kStages, kWarps, kMinCtas, kTeam>;
   const int smem = L::bytes(p.a.batch);
   if (!host::set_max_dynamic_smem(reinterpret_cast<const void *>(kern), L::bytes(kMaxBatch))) return NVFP4_ERR_CUDA;
-  int64_t grid = (int64_t)host::sm_count() * host::blocks_per_sm(reinterpret_cast<const void *>(kern), kThreads, smem);
+  // as for the largest batch: registers bound the residency at every batch, and the
+  // figures are kept per shared-memory size
+  int64_t grid =
+      (int64_t)host::sm_count() * host::blocks_per_sm(reinterpret_cast<const void *>(kern), kThreads, L::bytes(kMaxBatch));
   if (grid > max_grid()) grid = max_grid();
   const int64_t want = (total_bound + L::kTeams - 1) / L::kTeams;
   if (grid > want) grid = want < 1 ? 1 : want;

@@ -580,7 +580,7 @@ class PagedKVCache:
                 raise ValueError(f"{name}: an fp32 tensor of one element is wanted")
         _same_device(k_q, k_sf, k_gs, v_q, v_sf, v_gs)
         self.k_q, self.k_sf, self.k_gs, self.v_q, self.v_sf, self.v_gs = k_q, k_sf, k_gs, v_q, v_sf, v_gs
-        self._need = {}                 # workspace bytes by (batch, max_query, q_heads)
+        self._need = {}                 # workspace bytes by (batch, max_query, q_heads), at most 256 of them
         self._captured = []             # workspaces that captured graphs point to
 
     @classmethod
@@ -674,6 +674,8 @@ class PagedKVCache:
             raise ValueError("lse: a contiguous fp32 [tokens, q_heads] tensor is wanted")
         need = self._need.get((batch, max_query, hq))
         if need is None:
+            if len(self._need) >= 256:
+                self._need.clear()
             need = self._need[batch, max_query, hq] = nvfp4_paged_attention_workspace_size(batch, max_query, hq,
                                                                                            self.heads, D)
         given = ws is not None

@@ -149,3 +149,12 @@ def test_buffers_that_a_kernel_would_leave_are_refused(calls):
     cache().attend(**a, ws=torch.empty(need, dtype=torch.uint8), dev_status=ok)
     L.add_rmsnorm_nvfp4(x, w, gs, dev_status=ok)
     assert len(calls) == 2
+
+
+def test_what_a_cache_keeps_per_shape_is_bounded(calls):
+    """A server's max_query and batch take many values; a cache that lives as long as
+    the server does not keep one entry for each."""
+    c, a = cache(), attend_args()
+    for n in range(3, 3000):
+        c.attend(**a, max_query=n)
+    assert len(c._need) <= 256 and len(calls) == 2997
