@@ -772,12 +772,8 @@ bool launch_combine(const DecodeArgs &p, cudaStream_t stream) {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Most rows of a sequence that the decode form takes (the accumulators leave
-// room for no more); sequences with more go to the prefill form.
-constexpr int kRowLimit = 32;
-
-// 8-row tiles of a row block that holds `rows` rows.
-int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+using kv::kRowLimit;
+using kv::tiles_for;
 
 // CTAs that the workspace is sized for: at most 4 per SM.
 int64_t max_grid() { return (int64_t)host::sm_count() * 4; }
@@ -862,7 +858,6 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   if (num_pages > 0 && (!k_q || !k_sf || !v_q || !v_sf)) return NVFP4_ERR_INVALID_ARG;
   const int group = q_heads / kv_heads;
   const int64_t rows = max_query * group;
-  const int cap = kRowLimit;
   // The lines of both forms fit 32 bits: row blocks are bounded by the queries
   // that there are, and an item takes its steps or tiles and what it costs besides.
   const int64_t keys = (int64_t)max_pages * page_size;
@@ -896,19 +891,16 @@ nvfp4_status nvfp4_paged_attention(const void *q, int64_t ld_q, int64_t tokens, 
   p.a.v8_out = aligned(out, 32);
   p.a.lse = lse;
   p.a.dev_status = dev_status;
-  p.row_cap = cap;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if (rows > cap) {
-    // A batch may hold sequences for either form, each of which takes its own; a
-    // single one, or a batch of twice the decode form's rows on average, goes to
-    // the prefill form whole: the second pair of launches (about 12 us) costs more
-    // than few rows lose there.
-    const bool one_form = batch == 1 || tokens * group >= 2 * (int64_t)cap * batch;
+  const kv::Forms forms =
+      kv::choose_forms(batch, tokens, max_query, group, kv_heads, keys, query_offsets != nullptr, host::sm_count());
+  p.row_cap = forms.row_cap;
+  if (forms.prefill) {
     const nvfp4_status st =
-        launch_prefill(p.a, head_dim, one_form ? 0 : cap, ws + decode_workspace(batch, rows, head_dim), stream);
-    if (st != NVFP4_OK || one_form) return st;
+        launch_prefill(p.a, head_dim, forms.row_cap, ws + decode_workspace(batch, rows, head_dim), stream);
+    if (st != NVFP4_OK || forms.row_cap == 0) return st;
   }
-  const int nt = tiles_for(rows);
+  const int nt = forms.row_cap / 8;
   const int64_t total_bound = (int64_t)batch * kv_heads * (steps_max + kItemSteps);
   if (head_dim == 64) {
     if (nt == 1) return run<64, 1, 3, 8, 2>(p, total_bound, ws, stream);

@@ -67,5 +67,41 @@ NVFP4_HD void item_part(int64_t c, int64_t per, int64_t start, int fixed, int st
   hi = (int)(b < 0 ? 0 : b > steps ? steps : b);
 }
 
+// ---- which form of the attention takes a sequence, by its rows (queries * group)
+
+// Most rows of a sequence that the decode form takes (the accumulators leave room
+// for no more).
+constexpr int kRowLimit = 32;
+
+// 8-row tiles of a row block that holds `rows` rows, at most kRowLimit.
+inline int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+// The decode form takes sequences of up to row_cap rows (0: is not launched), the
+// prefill form the others.
+struct Forms {
+  int row_cap;
+  bool prefill;
+};
+
+// From what the host knows: the batch, its tokens, the most queries of a sequence
+// and the most keys (the lengths are on the device).  A prefill tile costs the
+// same with 4 rows in use as with 128: 32 sequences of 16 Ki tokens beside a prompt of
+// 2048 take 387 us there (8 KV heads of 128, 4 heads each) against 133 in the decode
+// form, so a batch that may hold both is split.  The second pair of launches costs 6 to
+// 12 us where it has nothing to do, so one form takes all where few-row sequences can
+// waste no more than that: `5 tiles an SM`, each 1.3 us (D 128) or 2.4 us (D 256).
+//
+// A split call's decode form has a tile for single queries (or for the mean rows,
+// where these fit it): for the sequences above, 8 rows take 133 us and 32 rows 256.
+inline Forms choose_forms(int64_t batch, int64_t tokens, int64_t max_query, int group, int heads_kv, int64_t keys,
+                          bool offsets, int64_t sms) {
+  const int64_t most = (max_query < tokens ? max_query : tokens) * group;
+  if (most <= kRowLimit) return Forms{8 * tiles_for(most), false};
+  const int64_t few_row_tiles = batch * heads_kv * (keys / 128 + 4);
+  if (!offsets || group > kRowLimit || batch == 1 || few_row_tiles <= 5 * sms) return Forms{0, true};
+  const int64_t mean = (tokens * group + batch - 1) / batch;
+  return Forms{8 * tiles_for(mean <= kRowLimit && mean > group ? mean : group), true};
+}
+
 }  // namespace kv
 }  // namespace nvfp4

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 import oracle
+from tests._forms import choose_forms
 from tests._util import bf16_dev, to_dev, to_np
 from tests.test_gpu_serving import Case, bits_of, bf16_of, layer, nvmod, random_bf16, same, status_word, values
 
@@ -236,3 +237,46 @@ def test_append_rounds_correctly_over_the_whole_range(power, gain, pairs):
     ks = to_np(cache.k_sf.transpose(1, 2).reshape(-1, heads, D // 16)[:T].contiguous())
     same(kq, np.where(blocks[..., None], q_.reshape(T, heads, D // 16, 8), np.uint8(0)))
     same(ks, np.where(blocks, sf_.reshape(T, heads, D // 16), np.uint8(0)))
+
+
+# ---------------------------------------------------------------------------------------- both forms in one call
+MIXED = [
+    # D, hkv, group, page, decode lengths (one query each), others (length, queries)
+    (64, 2, 4, 16, [0, 1, 33, 4000, 17, 2500, 64, 700] * 5, [(900, 50)]),
+    (128, 2, 4, 64, [0, 1, 33, 5000, 17, 2500, 64, 700] * 5, [(900, 50)]),
+    (256, 2, 4, 32, [0, 1, 33, 3000, 17, 2500, 64, 700] * 5, [(900, 50)]),
+    (128, 1, 8, 64, [6000, 0, 129, 1] * 10, [(3000, 300), (70, 70), (0, 40)]),
+    (256, 1, 8, 64, [6000, 0, 129, 1] * 10, [(3000, 300), (20, 30)]),
+    (64, 1, 16, 32, [6000, 31, 0, 1] * 12, [(2000, 129), (40, 3)]),
+    (128, 1, 32, 48, [6000, 31, 0, 1] * 10, [(2000, 65), (40, 2)]),
+    (256, 1, 12, 16, [3000, 31, 0, 2000] * 12, [(2000, 65), (40, 2), (1500, 3)]),
+    (128, 2, 2, 16, [4000, 31, 0, 1] * 10, [(2000, 17), (40, 16), (900, 4), (900, 5)]),
+]
+
+
+@pytest.mark.parametrize("D,hkv,group,ps,decodes,others", MIXED)
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_batches_that_both_forms_share(D, hkv, group, ps, decodes, others, causal):
+    """Long and short single-query sequences beside prompts: the rule sends work to
+    both forms, and every row and sum is there."""
+    half = len(decodes) // 2                          # the prompts in the middle and at the end
+    lens = decodes[:half] + [n for n, _ in others[:1]] + decodes[half:] + [n for n, _ in others[1:]]
+    counts = [1] * half + [q for _, q in others[:1]] + [1] * (len(decodes) - half) + [q for _, q in others[1:]]
+    c = Case(sum(lens) + D, D, hkv, group, ps, lens, counts, causal)
+    cap, prefill = choose_forms(len(lens), sum(counts), c.max_query, group, hkv, c.table.shape[1] * ps,
+                                sms=torch.cuda.get_device_properties(0).multi_processor_count)
+    assert prefill and any(n and q * group <= cap for n, q in zip(lens, counts)) and \
+        any(n and q * group > cap for n, q in zip(lens, counts))
+    want, lse, mag = c.reference()
+    for dt, td in ((layer().OUT_F32, torch.float32), (layer().OUT_BF16, torch.bfloat16)):
+        ls = torch.full(lse.shape, 5.0, dtype=torch.float32, device="cuda")
+        out = torch.full(c.q.shape, float("nan"), dtype=td, device="cuda")
+        st = status_word()
+        c.run(out=out, out_dtype=dt, lse=ls, dev_status=st)
+        assert st.item() == 0 and not torch.isnan(out).any()
+        err = (out.double() - want).abs() - c.tolerance(want, mag, td)
+        assert err.max().item() <= 0, err.max().item()
+        empty = torch.isinf(lse)
+        assert torch.equal(empty, torch.isinf(ls)) and (out[empty] == 0).all()
+        assert ((ls - lse)[~empty].abs() <= 2e-4 + 2.0 ** -21 * lse[~empty].abs()).all()
+        assert torch.equal(c.run(out_dtype=dt), out)

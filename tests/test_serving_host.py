@@ -2,12 +2,14 @@
 what the layer refuses before a kernel could run.  CPU only: the library's calls are
 recorded instead of made."""
 import contextlib
+import random
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from nvfp4_w4a4_quantized_04_b200 import layer as L  # noqa: E402
+from tests._forms import choose_forms  # noqa: E402
 
 
 @pytest.fixture
@@ -158,3 +160,51 @@ def test_what_a_cache_keeps_per_shape_is_bounded(calls):
     for n in range(3, 3000):
         c.attend(**a, max_query=n)
     assert len(c._need) <= 256 and len(calls) == 2997
+
+
+@pytest.mark.parametrize("group,cap", [(1, 8), (4, 8), (8, 8), (12, 16), (16, 16), (32, 32)])
+def test_decode_sequences_beside_a_prompt_keep_their_form(group, cap):
+    """A prompt in the batch does not draw single-query sequences of long contexts
+    into the 128-row form, where a tile costs the same for 4 rows as for 128."""
+    for decodes in (1, 32, 63):
+        for prompt in (100, 2048, 8192):
+            got = choose_forms(decodes + 1, decodes + prompt, prompt, group, 8, 16384)
+            assert got[1] and got[0] >= group
+            if prompt > 100:
+                assert got == (cap, True)
+
+
+def test_every_sequence_has_a_form():
+    r = random.Random(3)
+    for _ in range(20000):
+        group, batch = r.choice((1, 2, 4, 5, 8, 16, 31, 32, 33, 64, 200)), r.choice((1, 2, 7, 64, 4096))
+        max_query = r.choice((1, 2, 4, 9, 33, 2048))
+        tokens = r.randrange(1, batch * max_query + 1)
+        keys, heads = r.choice((0, 16, 1024, 65536, 1 << 20)), r.choice((1, 8))
+        offsets = max_query > 1 or r.random() < 0.5
+        if not offsets:
+            tokens = batch
+        cap, prefill = choose_forms(batch, tokens, max_query, group, heads, keys, offsets)
+        most = min(max_query, tokens) * group
+        assert cap in (0, 8, 16, 32) and (prefill or most <= cap)            # none is left over
+        if cap and prefill:
+            assert group <= cap and batch > 1 and offsets
+        # one form where only one can have work, or where the other's launches cost more than they save
+        if most <= 32:
+            assert not prefill
+        if group > 32 or not offsets:
+            assert (cap == 0) == (group > 32) and prefill == (group > 32)
+        if batch == 1 and most > 32:
+            assert (cap, prefill) == (0, True)
+
+
+def test_prompts_alone_and_few_rows_alone():
+    assert choose_forms(64, 64, 1, 8, 4, 262144, False) == (8, False)        # decode
+    assert choose_forms(64, 64, 1, 4, 8, 16384, False) == (8, False)
+    assert choose_forms(32, 100, 4, 8, 4, 8192) == (32, False)               # verification
+    assert choose_forms(32, 100, 2, 8, 4, 8192) == (16, False)
+    assert choose_forms(1, 4096, 4096, 4, 8, 4096) == (0, True)              # a prompt
+    assert choose_forms(2, 1024, 512, 4, 8, 512) == (0, True)                # short ones: no second pair of launches
+    assert choose_forms(64, 256, 16, 8, 4, 16384) == (32, True)              # verification with a loose max_query
+    assert choose_forms(64, 64, 16, 8, 4, 16384) == (8, True)
+    assert choose_forms(1, 4, 64, 8, 4, 262144) == (32, False)               # fewer tokens than max_query says
