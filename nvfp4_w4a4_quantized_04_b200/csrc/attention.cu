@@ -820,8 +820,8 @@ extern "C" {
 
 size_t nvfp4_paged_attention_workspace_size(int batch, int64_t max_query, int q_heads, int kv_heads, int head_dim) {
   using namespace nvfp4::attn;
-  if (batch < 1 || batch > kMaxBatch || max_query < 1 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads ||
-      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+  if (batch < 1 || batch > kMaxBatch || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 4096 ||
+      max_query < 1 || max_query > 0x7FFFFFFF / q_heads || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   const int64_t rows = max_query * (q_heads / kv_heads);
   return (size_t)(decode_workspace(batch, rows, head_dim) +

@@ -208,3 +208,13 @@ def test_prompts_alone_and_few_rows_alone():
     assert choose_forms(64, 256, 16, 8, 4, 16384) == (32, True)              # verification with a loose max_query
     assert choose_forms(64, 64, 16, 8, 4, 16384) == (8, True)
     assert choose_forms(1, 4, 64, 8, 4, 262144) == (32, False)               # fewer tokens than max_query says
+
+
+def test_workspace_size_of_refused_shapes():
+    """0 for what the attention refuses, also where the rows would pass 64 bits."""
+    from nvfp4_w4a4_quantized_04_b200 import build, nvfp4_paged_attention_workspace_size as size
+    build.build()
+    assert size(1, 1 << 62, 8, 4, 128) == 0 and size(4096, 1 << 61, 64, 1, 256) == 0
+    assert size(1, 0x7FFFFFFF // 8 + 1, 8, 4, 128) == 0
+    assert size(1, 1, 8192, 4, 128) == 0
+    assert size(1, 0x7FFFFFFF // 4096, 4096, 4096, 64) > 0
