@@ -593,6 +593,8 @@ nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void *v, int64_t
  *                  aligned, needs no clearing.  Calls that may overlap (other
  *                  streams, other captured graphs) need workspaces of their own.
  *   K and V elements of unused rows of a page may hold anything.
+ * The size is that of the current device (its SM count): ask with the device of the
+ * call current.
  * The order of the sums depends only on the shapes and lengths: two calls with
  * the same inputs give the same bits.
  */

@@ -477,6 +477,10 @@ def _status(t):
 _HERE = contextlib.nullcontext()
 
 
+def _cuda(t: torch.Tensor) -> bool:
+    return t.get_device() >= 0
+
+
 def _on(t: torch.Tensor):
     """A context in which t's device is the current one (torch's own costs some
     microseconds even when it already is)."""
@@ -629,8 +633,12 @@ class PagedKVCache:
 
     def workspace(self, batch: int, max_query: int, q_heads: int) -> torch.Tensor:
         """A workspace for ``attend`` calls of up to these sizes on one stream."""
-        n = nvfp4_paged_attention_workspace_size(batch, max_query, q_heads, self.heads, self.head_dim)
-        return torch.empty(max(n, 1), dtype=torch.uint8, device=self.k_q.device)
+        return torch.empty(max(self._size(batch, max_query, q_heads), 1), dtype=torch.uint8, device=self.k_q.device)
+
+    def _size(self, batch: int, max_query: int, q_heads: int) -> int:
+        # by the SM count of the cache's device
+        with _on(self.k_q) if _cuda(self.k_q) else _HERE:
+            return nvfp4_paged_attention_workspace_size(batch, max_query, q_heads, self.heads, self.head_dim)
 
     def attend(self, q, seq_lens, page_table, query_offsets=None, max_query: Optional[int] = None, softmax_scale=None,
                causal: bool = True, out=None, out_dtype=OUT_BF16, lse=None, ws=None, dev_status=None):
@@ -676,8 +684,7 @@ class PagedKVCache:
         if need is None:
             if len(self._need) >= 256:
                 self._need.clear()
-            need = self._need[batch, max_query, hq] = nvfp4_paged_attention_workspace_size(batch, max_query, hq,
-                                                                                           self.heads, D)
+            need = self._need[batch, max_query, hq] = self._size(batch, max_query, hq)
         given = ws is not None
         if not given:
             ws = self.k_q.new_empty(max(need, 1))

@@ -218,3 +218,22 @@ def test_workspace_size_of_refused_shapes():
     assert size(1, 0x7FFFFFFF // 8 + 1, 8, 4, 128) == 0
     assert size(1, 1, 8192, 4, 128) == 0
     assert size(1, 0x7FFFFFFF // 4096, 4096, 4096, 64) > 0
+
+
+def test_workspace_sizes_are_those_of_the_caches_device(calls, monkeypatch):
+    """The size depends on the SM count of the current device, so the cache's device is
+    current while it is asked for."""
+    inside, sizes = [], []
+
+    @contextlib.contextmanager
+    def on(t):
+        inside.append(t)
+        yield
+        inside.pop()
+    monkeypatch.setattr(L, "_on", on)
+    monkeypatch.setattr(L, "_cuda", lambda t: True, raising=False)
+    monkeypatch.setattr(L, "nvfp4_paged_attention_workspace_size", lambda *a: sizes.append(len(inside)) or 512)
+    c = cache()
+    c.workspace(2, 3, 4)
+    c.attend(**attend_args(), max_query=3)
+    assert sizes == [1, 1]
