@@ -566,7 +566,8 @@ nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void *v, int64_t
  * tokens j that query t sees, with KV head h / (q_heads / kv_heads).
  * The products are f16 x f16 with fp32 sums: K and V exactly (e2m1 * e4m3 is
  * an f16), the softmax weights rounded to f16, the sums and the softmax in fp32:
- * a weight is as exact as an fp32 score lets it be.
+ * a weight is as exact as an fp32 score lets it be, and to 2^-11 of itself or 2^-25
+ * of the largest weight among the keys that one CTA takes.
  *   q              bf16 [tokens, q_heads, head_dim], token stride ld_q (% 8).
  *   query_offsets  nullable int32 [batch+1]: queries of sequence b are
  *                  [query_offsets[b], query_offsets[b+1]); non-decreasing,
