@@ -223,8 +223,9 @@ def nvfp4_grouped_gemm_w4a16(x, ld_x, x_rows, row_index, b_q, b_sf, b_gs, expert
 
 def nvfp4_gemm_set_wait_budget(cycles: int) -> int:
     """Main-loop wait budget of the grouped GEMM kernels in SM cycles (0 =
-    default): the one-CTA kernels (256- and 512-element stages) and the
-    two-block kernel; a switch for testing the timeout path."""
+    default): the one-CTA kernels (256- and 512-element stages), the two-block
+    kernel and the paged attention's prefill form; a switch for testing the
+    timeout path."""
     st = load_library().nvfp4_gemm_set_wait_budget(cycles)
     _check(st, "nvfp4_gemm_set_wait_budget")
     return st

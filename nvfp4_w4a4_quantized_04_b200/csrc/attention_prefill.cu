@@ -983,4 +983,10 @@ nvfp4_status launch_prefill(const Args &a, int D, int row_floor, uint8_t *ws, cu
 }
 
 }  // namespace attn
+namespace gemm {
+nvfp4_status set_wait_budget_prefill(long long cycles) {
+  return cudaMemcpyToSymbol(c_wait_budget, &cycles, sizeof(cycles)) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+}  // namespace gemm
+
 }  // namespace nvfp4

@@ -392,7 +392,8 @@ extern "C" nvfp4_status nvfp4_gemm_set_wait_budget(int64_t cycles) {
   const long long v = cycles == 0 ? gemm::kWaitBudgetCycles : (long long)cycles;
   if (cudaMemcpyToSymbol(gemm::c_wait_budget, &v, sizeof(v)) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (gemm::set_wait_budget_k512(v) != NVFP4_OK) return NVFP4_ERR_CUDA;
-  return gemm::set_wait_budget_w2(v);
+  if (gemm::set_wait_budget_w2(v) != NVFP4_OK) return NVFP4_ERR_CUDA;
+  return gemm::set_wait_budget_prefill(v);
 }
 
 extern "C" nvfp4_status nvfp4_gemm_select_kernel(int mode) {

@@ -831,6 +831,8 @@ nvfp4_status launch_grouped_gemm_w2(const uint8_t *a_q, const uint8_t *a_sf, con
                                     const HQuantOut *hq, bool mx, bool deep, int32_t *dev_status,
                                     cudaStream_t stream);
 nvfp4_status set_wait_budget_w2(long long cycles);
+// The copy of the attention's prefill form (attention_prefill.cu).
+nvfp4_status set_wait_budget_prefill(long long cycles);
 
 // The pair kernel's launch (gemm_pair.cu).  Requires N % 256 == 0.
 nvfp4_status launch_grouped_gemm_pair(const uint8_t *a_q, const uint8_t *a_sf, const float *a_gs,

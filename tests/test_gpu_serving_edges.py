@@ -280,3 +280,27 @@ def test_attention_batches_that_both_forms_share(D, hkv, group, ps, decodes, oth
         assert torch.equal(empty, torch.isinf(ls)) and (out[empty] == 0).all()
         assert ((ls - lse)[~empty].abs() <= 2e-4 + 2.0 ** -21 * lse[~empty].abs()).all()
         assert torch.equal(c.run(out_dtype=dt), out)
+
+
+@pytest.mark.parametrize("D,hkv,group,lens,queries", [(64, 4, 4, [700], [700]), (128, 8, 4, [1500, 300], [1500, 80]),
+                                                      (256, 2, 8, [1000, 90, 400], [300, 90, 40])])
+def test_attention_prefill_waits_give_up_and_report(D, hkv, group, lens, queries):
+    """A wait that runs out ends the kernel with a status, outside the rows' neighbours
+    and with a context that stays usable: the next call is right again."""
+    L, nv = layer(), nvmod()
+    c = Case(30 + D, D, hkv, group, 64, lens, queries, True)
+    T, H = c.q.shape[:2]
+    want = c.run(out_dtype=L.OUT_F32)
+    wide = torch.full((T + 8, H, D), 3.0, device="cuda")
+    st = status_word()
+    torch.cuda.synchronize()
+    nv.nvfp4_gemm_set_wait_budget(1)
+    try:
+        c.run(out=wide[4:T + 4], out_dtype=L.OUT_F32, dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == nv.ERR_TIMEOUT
+    finally:
+        nv.nvfp4_gemm_set_wait_budget(0)
+    assert (wide[:4] == 3).all() and (wide[T + 4:] == 3).all()
+    st.zero_()
+    assert torch.equal(c.run(out_dtype=L.OUT_F32, dev_status=st), want) and st.item() == 0
