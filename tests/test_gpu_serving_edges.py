@@ -10,7 +10,7 @@ import pytest
 import oracle
 from tests._forms import choose_forms
 from tests._util import bf16_dev, to_dev, to_np
-from tests.test_gpu_serving import Case, bits_of, bf16_of, layer, nvmod, random_bf16, same, status_word, values
+from tests.test_gpu_serving import FEW_ROWS, Case, bits_of, bf16_of, layer, nvmod, random_bf16, same, status_word, values
 
 pytestmark = pytest.mark.gpu
 
@@ -304,3 +304,81 @@ def test_attention_prefill_waits_give_up_and_report(D, hkv, group, lens, queries
     assert (wide[:4] == 3).all() and (wide[T + 4:] == 3).all()
     st.zero_()
     assert torch.equal(c.run(out_dtype=L.OUT_F32, dev_status=st), want) and st.item() == 0
+
+
+# ---------------------------------------------------------------------------------------- exact scores
+def exact_scores(c, seed):
+    """Queries of +-1, +-2 and keys of +-0.5, +-1, +-2: every partial sum of a score is
+    a multiple of 0.5 below 2^11, exact in fp32.  Unused rows keep their garbage."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    used = c.t["k_sf"][..., :1] != 0xFF
+    table = torch.tensor([1, 2, 4, 9, 10, 12], dtype=torch.uint8, device="cuda")
+    nib = table[torch.randint(0, 6, (*c.t["k_q"].shape, 2), generator=g, device="cuda")]
+    c.t["k_q"].copy_(torch.where(used, nib[..., 0] | nib[..., 1] << 4, c.t["k_q"]))
+    c.t["k_sf"].copy_(torch.where(used, torch.full_like(c.t["k_sf"], 0x38), c.t["k_sf"]))
+    c.kgs.fill_(1.0)
+    sizes = torch.tensor([1.0, 2.0, -1.0, -2.0], device="cuda").to(torch.bfloat16)
+    c.q.copy_(sizes[torch.randint(0, 4, c.q.shape, generator=g, device="cuda")])
+
+
+PEAKED = [(D, hkv, group, ps, lens, queries, True) for D, hkv, group, ps, lens, queries in FEW_ROWS] + [
+    (64, 2, 4, 32, [900, 333], None, True), (128, 2, 4, 32, [900, 333], None, True), (256, 2, 4, 32, [900, 333], None, True),
+    (128, 8, 4, 64, [2048], [2048], True), (64, 8, 4, 32, [2048], [2048], True), (256, 4, 4, 64, [1500], [1500], True),
+    (128, 2, 8, 128, [1500, 900, 1800], [700, 900, 1], True), (256, 1, 2, 64, [9000, 200], [130, 65], False),
+    (64, 1, 16, 16, [130, 2000, 17], [2, 3, 17], False)]
+
+
+@pytest.mark.parametrize("D,hkv,group,ps,lens,queries,causal", PEAKED)
+@pytest.mark.parametrize("scale", [0.02, 0.3, 2.0])
+def test_attention_of_exact_scores(D, hkv, group, ps, lens, queries, causal, scale):
+    """From even weights to one key that takes all, with scores that carry no error into
+    the softmax, so that a wrong maximum, rescale or join shows.  The tolerance: the
+    scaling's roundings (factor, product, difference: 2^-21 of the largest score), the
+    weights' f16 rounding (2^-11, or 2^-25 absolute against a maximum of 1 at least),
+    exp2 (2^-22) and N/16 + 64 additions; the sum's logarithm has all but the f16 part."""
+    L = layer()
+    c = Case(sum(lens) + D, D, hkv, group, ps, lens, queries, causal)
+    exact_scores(c, 77 + D)
+    plain = c.q
+    stretch = scale * D ** 0.5                                     # the reference scales by D^-0.5
+    want, lse, mag = c.reference(q=plain.double() * stretch)
+    ls = torch.full(lse.shape, 5.0, dtype=torch.float32, device="cuda")
+    st = status_word()
+    out = c.run(out_dtype=L.OUT_F32, softmax_scale=scale, lse=ls, dev_status=st)
+    assert st.item() == 0 and not torch.isnan(out).any()
+    n = max(lens)
+    top = scale * 4 * D                                            # no score is larger
+    top = min(top, scale * 2.1 * D ** 0.5 * 7)                     # nor, for these values, beyond 7 deviations
+    ds = 2.0 ** -21 * top + 2.0 ** -22 + (n / 16 + 64) * 2.0 ** -24
+    err = (out.double() - want).abs() - (mag * (2.0 ** -11 + 2 * ds) + n * 2.0 ** -25 * c.vmax + out.abs() * 2.0 ** -24)
+    assert err.max().item() <= 0, err.max().item()
+    empty = torch.isinf(lse)
+    assert torch.equal(empty, torch.isinf(ls)) and (out[empty] == 0).all()
+    assert ((ls - lse)[~empty].abs() <= ds + 2.0 ** -22 * lse[~empty].abs() + 2.0 ** -23).all()
+
+
+# ---------------------------------------------------------------------------------------- into the GEMM
+@pytest.mark.parametrize("rows,K,N", [(1, 256, 256), (70, 512, 256), (128, 256, 512), (300, 1024, 512)])
+def test_norm_feeds_the_projection(rows, K, N):
+    """The norm's output goes into the W4A4 GEMM as it is: the same result as that of the
+    quantized y, whatever the buffers' padding rows held."""
+    L = layer()
+    torch.manual_seed(rows)
+    x, r = (torch.randn(rows, K, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = (1 + 0.1 * torch.randn(K, device="cuda")).to(torch.bfloat16)
+    wp = L.quantize((0.05 * torch.randn(N, K, device="cuda")).to(torch.bfloat16))
+    gs = torch.tensor([6.0 / 2688], device="cuda")
+    y = torch.empty_like(x)
+    packed = L.empty_packed(rows, K)
+    packed.q.fill_(0x7F)
+    packed.sf.fill_(0x7F)                                          # NaN
+    st = status_word()
+    packed, _, _ = L.add_rmsnorm_nvfp4(x, w, gs, residual=r, out=packed, y=y, dev_status=st)
+    got = L.grouped_gemm(packed, wp, N, L.OUT_F32, dev_status=st)
+    want = L.grouped_gemm(L.quantize(y, global_scale=gs), wp, N, L.OUT_F32, dev_status=st)
+    assert st.item() == 0 and torch.isfinite(got).all() and torch.equal(got, want)
+    # the buffers again, with scales of their own: the calibrated one is as it was
+    L.quantize(x, out=packed)
+    assert gs.item() == np.float32(6.0 / 2688) and packed.gs is not gs
+    assert torch.equal(L.grouped_gemm(packed, wp, N, L.OUT_F32), L.grouped_gemm(L.quantize(x), wp, N, L.OUT_F32))
