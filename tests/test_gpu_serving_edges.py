@@ -382,3 +382,49 @@ def test_norm_feeds_the_projection(rows, K, N):
     L.quantize(x, out=packed)
     assert gs.item() == np.float32(6.0 / 2688) and packed.gs is not gs
     assert torch.equal(L.grouped_gemm(packed, wp, N, L.OUT_F32), L.grouped_gemm(L.quantize(x), wp, N, L.OUT_F32))
+
+
+# ---------------------------------------------------------------------------------------- captured
+@pytest.mark.parametrize("D,hkv,group,lens,counts", [
+    (128, 8, 4, [1500, 0, 900], [1500, 0, 300]),                                       # the prefill form
+    (128, 2, 4, [4000, 33, 1, 2500] * 10 + [900], [1] * 40 + [60]),                    # both forms
+    (256, 2, 4, [3000, 33, 1, 2500] * 10 + [900], [1] * 40 + [60]),
+    (64, 4, 8, [6000, 33, 1, 700] * 10 + [900], [1] * 40 + [60])])
+def test_attention_in_graphs_of_either_form_takes_new_lengths(D, hkv, group, lens, counts):
+    """Captured once and replayed with other lengths, offsets and queries inside the
+    captured sizes, on a padded batch whose last rows no sequence has, with pages that
+    two sequences share: the same bits as a plain call."""
+    c = Case(40 + D, D, hkv, group, 64, lens, counts, True)
+    pad, T = 9, sum(counts)
+    c.table[1] = c.table[0]                                        # a shared prefix
+    q = torch.randn(T + pad, *c.q.shape[1:], device="cuda").to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = c.cache.workspace(len(lens), c.max_query, q.shape[1])
+    st = status_word()
+
+    def run(out, lse, ws):
+        c.cache.attend(q, c.seq_lens, c.table, query_offsets=c.offsets, max_query=c.max_query, out=out, lse=lse, ws=ws,
+                       dev_status=st)
+    run(out, lse, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out, lse, ws)
+    for turn in range(3):
+        q.copy_(torch.randn(q.shape, device="cuda"))
+        if turn:
+            less = [n if i % 3 else max(0, n - 17 * turn) for i, n in enumerate(lens)]
+            less[1] = less[0]
+            fewer = [max(0, n - turn) if i % 4 == 0 else n for i, n in enumerate(counts)]
+            c.seq_lens.copy_(torch.tensor(less, dtype=torch.int32))
+            c.offsets.copy_(torch.tensor([0] + list(np.cumsum(fewer)), dtype=torch.int32))
+        out.fill_(3.0)
+        lse.fill_(4.0)
+        graph.replay()
+        want, wl = torch.full_like(out, 3.0), torch.full_like(lse, 4.0)
+        run(want, wl, None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl) and st.item() == 0
+        last = int(c.offsets[-1])
+        assert (out[last:] == 3).all() and (lse[last:] == 4).all() and last < T + pad
+        assert not torch.isnan(out).any()
