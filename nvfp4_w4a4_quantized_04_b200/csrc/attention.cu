@@ -44,12 +44,14 @@
 // CTAs share is joined by a second kernel from (max, sum, unnormalized O) parts
 // in the workspace.
 //
-// Measured, with the join: 64 sequences of up to 16 Ki tokens, 8 KV heads of 128
-// and 4 heads each: 135 us, 4.7 TB/s (72 % of a copy's rate); one of 256 Ki
-// tokens, 4 KV heads of 256 and 8 heads each: 68 us, 4.4 TB/s; 32 of 8 Ki with 4
-// queries of 8 heads on 4 of 256: 86 us.  What bounds it is the issue of the
-// conversions (about 600 warp instructions a step at D 128); more warps a SM
-// with fewer registers each are slower.
+// Measured, with the join, in replayed graphs: 64 sequences of up to 16 Ki tokens, 8 KV
+// heads of 128 and 4 heads each: 136 us, 4.7 TB/s (72 % of a copy's rate; 140 to 148
+// in plain calls on other boxes); one of 256 Ki tokens, 4 KV heads of 256 and 8 heads
+// each: 69 us, 4.4 TB/s; 32 of 8 Ki with 4 queries of 8 heads on 4 of 256: 86 us.  No
+// pipe is full (at D 128 issue slots 63 %, ALU with the conversions 52 %, DRAM 58 %,
+// tensor 26 %): the stalls are fixed latencies and the math pipe, with four warps a
+// scheduler at D 128 and two at D 256; more warps a SM with fewer registers each are
+// slower.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>

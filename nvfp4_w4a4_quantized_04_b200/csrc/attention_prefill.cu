@@ -48,11 +48,11 @@
 //    a proxy fence, or the next bulk copy passes reads that are still in flight.
 //
 // Measured, all three kernels: 4096 queries of 32 heads on 8 of 128 over their own
-// keys: 217 us, 633 TFLOP/s (39 % of cuBLAS's bf16 rate), bound by the softmax
+// keys: 221 us, 621 TFLOP/s (38 % of cuBLAS's bf16 rate), bound by the softmax
 // warps: of 2470 cycles a tile they spend 1500 in the weights (the exponentials
 // alone take 1024) and the rest waiting for S, loading it, voting and storing P;
 // an item costs about 13000 cycles besides.  2048 queries of 32 heads on 4 of 256
-// over 32 Ki keys: 2070 us, 1030 TFLOP/s (64 %), bound by shared-memory bandwidth:
+// over 32 Ki keys: 2098 us, 1015 TFLOP/s (63 %), bound by shared-memory bandwidth:
 // 1500 us without the conversion and its stores.
 #include "attention.cuh"
 #include "attention_internal.cuh"

@@ -10,17 +10,19 @@
 // kernel from the memory rate.  The block encode is the one of nvfp4_quantize
 // with a given global scale.
 //
-// Bound by HBM: 2 bytes in and 9/16 out per element of k and v, 2 + 2 per
+// Traffic: 2 bytes in and 9/16 out per element of k and v, 2 + 2 per
 // element of q.  A thread owns 32 elements of one token: the two 16-element
 // blocks that the rotation of halves couples (block u and u + rot/32), or two
 // neighbouring ones.  It keeps its 32 cosines and sines in registers and walks
-// over the heads, so the table is read once per token instead of once per
-// head; the host cuts the heads into chunks until the grid fills the GPU, so
-// that a decode step's few tokens still spread over all SMs.
+// over a chunk of the heads, so that long prompts read the table once per token
+// and chunk; the host halves the chunk until there are 1024 threads an SM, so that
+// a decode step's few tokens still spread over all SMs (about 1000 tokens end at
+// one head a thread).
 //
-// Measured: 16384 tokens of 32 + 2 x 4 heads of 256: 157 us, 4.5 TB/s (69 % of a
-// copy's rate; the dequantization of the pool that the timed call also makes is
-// in it); 64 tokens 12 us with it, the latency of slot, table, load and store.
+// Measured: 16384 tokens of 32 + 2 x 4 heads of 256: 139 us, 4.5 TB/s (68 % of a
+// copy's rate), bound by the loads in flight of 12 warps an SM (168 registers; the
+// long scoreboard is the top stall, issue slots 49 %); 1037 tokens of 32 + 2 x 8
+// heads of 128: 17 us; 64 tokens 6.3 us, the latency of slot, table, load and store.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

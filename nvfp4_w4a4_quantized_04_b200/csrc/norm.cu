@@ -22,12 +22,14 @@
 // the order of the sum.  The root's power of two goes into r first, so that the
 // product with w leaves fp32's range only where y does; below 2^-100, or 2^-100 |w|,
 // what a subnormal drops makes y less exact.  (Such elements in 64 bits cost 270 to
-// 290 us instead of 217 for the large case: the test for them also finds the zeros
+// 290 us instead of 217 for 32768 rows: the test for them also finds the zeros
 // that a residual leaves, about one in 10^3.  Products as (r root) w: 223.)
 //
-// Measured with a residual, K 5120: 32768 rows to E4M3 215 us, 5.5 TB/s (84 % of a
-// copy's rate); 64 rows 6.2 us, which is one row's latency (load, two block
-// reductions, store) and the launch.
+// Measured with a residual, K 5120: 32768 rows to E4M3 217 us in replayed graphs, 5.4
+// TB/s (82 % of a copy's rate; 237 in plain calls); 4096 rows to NVFP4 33 us; 64 rows
+// 6.3 us, which is one row's latency (load, two block reductions, store) and the launch.
+// Four CTAs of ten warps an SM by registers; issue slots 69 %, stalls on loads and at
+// the reductions' barriers.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
