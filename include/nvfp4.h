@@ -430,15 +430,16 @@ nvfp4_status nvfp4_gemm_select_kernel(int mode);
 /*
  * nvfp4_gemm_set_wait_budget -- a testing switch for the failure path of the
  * one-CTA grouped GEMM kernels (nvfp4_gemm_select_kernel modes 0, 1, 3 and
- * 4) and of the paged attention's prefill form (not part of the pages' method;
- * the attention then leaves the outputs of the CTA's items unwritten).  Every wait of the kernel's main loop on a ring,
- * scale or accumulator barrier gives up after this many SM clock cycles: it
- * raises the CTA's abort flag, writes NVFP4_ERR_TIMEOUT to dev_status, and
- * every role leaves its loop.  The closing waits for copies and MMAs still in
- * flight keep the full budget, so the kernel ends cleanly and the context
- * stays usable.  cycles = 0 restores the default (4e9 cycles, about 2 s); a
- * test sets 1 to force the timeout.  Process-wide, synchronous; call it
- * between launches.  Returns NVFP4_ERR_INVALID_ARG for cycles < 0.
+ * 4) and of the paged attention's prefill form (not part of the pages' method).
+ * Every wait of the kernel's main loop on a ring, scale or accumulator barrier
+ * gives up after this many SM clock cycles: it raises the CTA's abort flag,
+ * writes NVFP4_ERR_TIMEOUT to dev_status, and every role leaves its loop (the
+ * attention's outputs of that CTA are then unspecified).  The closing waits for
+ * copies and MMAs still in flight keep the full budget, so the kernel ends
+ * cleanly and the context stays usable.  cycles = 0 restores the default (4e9
+ * cycles, about 2 s); a test sets 1 to force the timeout.  Process-wide,
+ * synchronous; call it between launches.  Returns NVFP4_ERR_INVALID_ARG for
+ * cycles < 0.
  */
 nvfp4_status nvfp4_gemm_set_wait_budget(int64_t cycles);
 

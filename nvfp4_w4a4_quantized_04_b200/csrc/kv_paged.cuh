@@ -89,7 +89,7 @@ struct Forms {
 // 2048 take 387 us there (8 KV heads of 128, 4 heads each) against 133 in the decode
 // form, so a batch that may hold both is split.  The second pair of launches costs 6 to
 // 12 us where it has nothing to do, so one form takes all where few-row sequences can
-// waste no more than that: `5 tiles an SM`, each 1.3 us (D 128) or 2.4 us (D 256).
+// waste no more than that: up to 5 tiles an SM, each 1.3 us (D 128) or 2.4 us (D 256).
 //
 // A split call's decode form has a tile for single queries (or for the mean rows,
 // where these fit it): for the sequences above, 8 rows take 133 us and 32 rows 256.
