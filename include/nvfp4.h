@@ -540,7 +540,7 @@ nvfp4_status nvfp4_add_rmsnorm_quantize(const void *x, int64_t ld_x, const void 
  *                 tokens with one slot leave codes and scales of either there
  *                 (finite values, which ones is not defined).
  *   q, q_out      nullable bf16 [tokens, q_heads, head_dim], strides ld_q,
- *                 ld_qo: rotated copy; q_out may be q itself, in place.
+ *                 ld_qo: rotated copy; q_out may be q itself (same stride).
  *   rope          fp32 [rope_rows, rot_dim]: per position rot_dim/2 cosines,
  *                 then rot_dim/2 sines; 16-byte aligned.  rot_dim % 32 == 0,
  *                 <= head_dim; 0 = no rotation (q is copied).

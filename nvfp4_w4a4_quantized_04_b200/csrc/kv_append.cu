@@ -256,6 +256,7 @@ extern "C" nvfp4_status nvfp4_kv_append(const void *k, int64_t ld_k, const void 
   if (ld_k < nkv || ld_v < nkv || ld_k % 8 || ld_v % 8 || (q && (ld_q < nq || ld_qo < nq || ld_q % 8 || ld_qo % 8)))
     return NVFP4_ERR_INVALID_ARG;
   if (tokens == 0) return NVFP4_OK;
+  if (tokens > 1 && q && q_out == q && ld_qo != ld_q) return NVFP4_ERR_INVALID_ARG;     // in place only row by row
   if (!k || !v || !slots || !k_gs || !v_gs || (rot_dim > 0 && !positions) || (q && !q_out)) return NVFP4_ERR_INVALID_ARG;
   if (num_pages > 0 && (!k_q || !k_sf || !v_q || !v_sf)) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_q, 16) ||

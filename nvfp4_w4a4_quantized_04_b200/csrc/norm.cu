@@ -264,6 +264,9 @@ extern "C" nvfp4_status nvfp4_add_rmsnorm_quantize(const void *x, int64_t ld_x, 
       (residual_out && (ld_ro < K || ld_ro % 8)))
     return NVFP4_ERR_INVALID_ARG;
   if (rows == 0) return NVFP4_OK;
+  // in place only row by row
+  if (rows > 1 && residual_out && ((residual_out == x && ld_ro != ld_x) || (residual_out == residual && ld_ro != ld_res)))
+    return NVFP4_ERR_INVALID_ARG;
   if (!x || !weight || !aligned(x, 16) || !aligned(weight, 16) || !aligned(residual, 16) ||
       !aligned(residual_out, 16) || !aligned(y, 16))
     return NVFP4_ERR_INVALID_ARG;

@@ -237,3 +237,29 @@ def test_workspace_sizes_are_those_of_the_caches_device(calls, monkeypatch):
     c.workspace(2, 3, 4)
     c.attend(**attend_args(), max_query=3)
     assert sizes == [1, 1]
+
+
+def test_in_place_outputs_of_another_stride_are_refused():
+    """r may go where x or the residual is, and the rotated queries where the queries are,
+    row by row: with another stride one row's output lies in a row still to be read."""
+    import nvfp4_w4a4_quantized_04_b200 as nv
+    from nvfp4_w4a4_quantized_04_b200 import build
+    from tests.test_kv_paged import APPEND, APPEND_OK, F, NORM, NORM_OK
+    build.build()
+    lib = nv.load_library()
+    far = 1 << 24                                     # never dereferenced: the checks fail first
+
+    def norm(**change):
+        a = dict(NORM_OK, x=F, res=2 * F, w=3 * F, ro=far, q=5 * F, sf=6 * F, scale=7 * F, **{})
+        a.update(change)
+        return lib.nvfp4_add_rmsnorm_quantize(*[a[n] for n in NORM])
+
+    def append(**change):
+        a = dict(APPEND_OK, q=F, qo=F)
+        a.update(change)
+        return lib.nvfp4_kv_append(*[a[n] for n in APPEND])
+    assert norm(ro=F, ld_ro=264) == nv.ERR_INVALID_ARG
+    assert norm(ro=F, ld_x=512) == nv.ERR_INVALID_ARG
+    assert norm(ro=2 * F, ld_ro=264) == nv.ERR_INVALID_ARG
+    assert append(ld_qo=2048) == nv.ERR_INVALID_ARG
+    assert append(ld_q=2048) == nv.ERR_INVALID_ARG
